@@ -9,9 +9,19 @@ built, or the device is not a B200, calls raise.
     C = qgemm_w8a8(A, W)                                         # int8 x int8 -> int32
     C = qgemm_w2a8(A, Wq)                                        # int8 x packed int2 -> int32
     Wq = quant_pack_int4(codes)                                  # uint8 [N,K] -> int32 [N,K/8]
+
+An 8-bit gated feed-forward block from 16-bit activations X, and its 16-bit form with gradients:
+
+    Q, sa = quant_int8_tokens(X)                                 # int8 [M,K], fp32 [M]
+    H = qgemm_w8a8_gated(Q, Wg, Wu, sa, sg, su, act="silu")      # act(gate) * up
+    Q, sa = quant_int8_tokens(H)
+    Y = qgemm_w8a8_scaled(Q, Wd, sa, sd, bias)                   # scales per token and channel
+    H, G, U = qgemm_dense_gated(X, Wg, Wu, save_preact=True)
+    dX, dWg, dWu = qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,6 +43,9 @@ QGEMM_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 OP_W4A16, OP_W8A8, OP_W2A8, OP_DENSE_F16, OP_W4A16_INTERLEAVED = 0, 1, 2, 3, 4
 OP_W2A8_INTERLEAVED = 5
 PATH_AUTO, PATH_GEMV, PATH_TC, PATH_STREAM = 0, 1, 2, 3
+DTYPE_F16, DTYPE_BF16 = 0, 1
+# activations of the gated feed-forward block by name (qg_act)
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 # every symbol include/qgemm.h declares
 EXPORTS = (
@@ -40,6 +53,8 @@ EXPORTS = (
     "qgemm_w4a16_splitk_f32_noalloc", "qgemm_w4a16_host", "qgemm_w4a16_host_workspace_bytes",
     "qgemm_w8a8", "qgemm_w2a8", "qgemm_w2a8_interleaved", "qgemm_dense_f16", "quant_pack_int4",
     "quant_rtn_int4", "qgemm_w8a8_requant",
+    "quant_int8_tokens", "qgemm_w8a8_scaled", "qgemm_w8a8_gated", "qgemm_dense_gated",
+    "qgemm_dense_gated_backward", "qgemm_dense_gated_backward_workspace_bytes",
     "quant_pack_int2", "quant_pack_int2_interleaved", "qgemm_plan", "qgemm_set_config", "qgemm_tune", "qgemm_save_configs",
     "qgemm_load_configs", "qgemm_clear_configs", "qgemm_sync_check", "qgemm_selftest_bounded_wait",
     "qgemm_status_string",
@@ -97,6 +112,13 @@ def lib() -> ctypes.CDLL:
         L.quant_pack_int4.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp]
         L.quant_pack_int2.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp]
         L.quant_pack_int2_interleaved.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, vp]
+        L.quant_int8_tokens.argtypes = [vp, vp, vp, i32, i32, i32, vp]
+        L.qgemm_w8a8_scaled.argtypes = [vp] * 6 + [i32] * 4 + [vp]
+        L.qgemm_w8a8_gated.argtypes = [vp] * 7 + [i32] * 5 + [vp]
+        L.qgemm_dense_gated.argtypes = [vp] * 6 + [i32] * 5 + [vp]
+        L.qgemm_dense_gated_backward.argtypes = [vp] * 9 + [i32] * 5 + [vp, ctypes.c_size_t, vp]
+        L.qgemm_dense_gated_backward_workspace_bytes.argtypes = [i32, i32, i32]
+        L.qgemm_dense_gated_backward_workspace_bytes.restype = ctypes.c_size_t
         L.qgemm_plan.argtypes = [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(Config)]
         L.qgemm_set_config.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(Config)]
         L.qgemm_tune.argtypes = [i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp,
@@ -112,7 +134,8 @@ def lib() -> ctypes.CDLL:
         L.qgemm_version.restype = i32
         for name in EXPORTS:
             if name not in ("qgemm_status_string", "qgemm_clear_configs", "qgemm_version",
-                            "qgemm_w4a16_workspace_bytes", "qgemm_w4a16_host_workspace_bytes"):
+                            "qgemm_w4a16_workspace_bytes", "qgemm_w4a16_host_workspace_bytes",
+                            "qgemm_dense_gated_backward_workspace_bytes"):
                 getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -417,6 +440,200 @@ def quant_pack_int2_interleaved(vals, out=None, stream=None):
     _check(lib().quant_pack_int2_interleaved(_ptr(vals), _ptr(out), 0, N, K, -1, 1, 0,
                                              _stream(stream)), "quant_pack_int2_interleaved")
     return out
+
+
+# ---- 8-bit activations with scales; the gated feed-forward block ---------------------------------
+
+def _operand(t, dtype, shape, name, device):
+    """As _need, with the whole shape and the device given."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _half_type(t, name):
+    """qg_dtype of a tensor, or of a torch.dtype."""
+    torch = _torch()
+    dtype = getattr(t, "dtype", t)
+    if dtype == torch.float16:
+        return DTYPE_F16
+    if dtype == torch.bfloat16:
+        return DTYPE_BF16
+    raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _on(device, stream):
+    """(context, stream handle) of a call on `device`: inside the context it is the current
+    device and `stream` its current stream, so that what the call allocates belongs to the
+    stream that writes it."""
+    torch = _torch()
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        if device.index == torch.cuda.current_device():
+            return contextlib.nullcontext(), handle
+        return torch.cuda.device(device), handle
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def quant_int8_tokens(X, Q=None, scales=None, stream=None):
+    """X fp16/bf16 [M,K] -> (Q int8 [M,K], scales fp32 [M]): amax = max |x| of the token,
+    scale = amax / 127, code = rint(x * (127 / amax)) (rule in include/qgemm.h)."""
+    torch = _torch()
+    dt = _half_type(X, "X")
+    _need(X, X.dtype, 2, "X")
+    M, K = X.shape
+    scope, handle = _on(X.device, stream)
+    with scope:
+        if Q is None:
+            Q = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        if scales is None:
+            scales = torch.empty((M,), dtype=torch.float32, device=X.device)
+        st = lib().quant_int8_tokens(X.data_ptr(), _operand(Q, torch.int8, (M, K), "Q", X.device),
+                                     _operand(scales, torch.float32, (M,), "scales", X.device),
+                                     M, K, dt, handle)
+    _check(st, "quant_int8_tokens")
+    return Q, scales
+
+
+def qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias=None, C=None, out_dtype=None, stream=None):
+    """A int8 [M,K], W int8 [N,K], a_scales fp32 [M], w_scales fp32 [N], bias [N] or None ->
+    C [M,N] = a_scales[m] * w_scales[n] * (A . W^T) (+ bias), in the type of C or of `out_dtype`
+    (fp16, the default, or bf16; bias has it too)."""
+    torch = _torch()
+    _need(A, torch.int8, 2, "A")
+    _need(W, torch.int8, 2, "W")
+    (M, K), N, dev = A.shape, W.shape[0], A.device
+    if out_dtype is None:
+        out_dtype = torch.float16 if C is None else C.dtype
+    dt = _half_type(out_dtype, "out_dtype")
+    scope, handle = _on(dev, stream)
+    with scope:
+        if C is None:
+            C = torch.empty((M, N), dtype=out_dtype, device=dev)
+        st = lib().qgemm_w8a8_scaled(
+            A.data_ptr(), _operand(W, torch.int8, (N, K), "W", dev),
+            _operand(a_scales, torch.float32, (M,), "a_scales", dev),
+            _operand(w_scales, torch.float32, (N,), "w_scales", dev),
+            None if bias is None else _operand(bias, out_dtype, (N,), "bias", dev),
+            _operand(C, out_dtype, (M, N), "C", dev), M, N, K, dt, handle)
+    _check(st, "qgemm_w8a8_scaled")
+    return C
+
+
+def qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H=None, act: str = "silu",
+                     out_dtype=None, stream=None):
+    """A int8 [M,K]; Wg, Wu int8 [F,K]; a_scales fp32 [M]; g_scales, u_scales fp32 [F] ->
+    H [M,F] = act(gate) * up in the type of H or of `out_dtype` (fp16, the default, or bf16),
+    gate and up being the scaled products with Wg and Wu. act: silu, gelu or gelu_tanh."""
+    torch = _torch()
+    _need(A, torch.int8, 2, "A")
+    _need(Wg, torch.int8, 2, "Wg")
+    (M, K), F, dev = A.shape, Wg.shape[0], A.device
+    if out_dtype is None:
+        out_dtype = torch.float16 if H is None else H.dtype
+    dt, code = _half_type(out_dtype, "out_dtype"), _activation(act)
+    scope, handle = _on(dev, stream)
+    with scope:
+        if H is None:
+            H = torch.empty((M, F), dtype=out_dtype, device=dev)
+        st = lib().qgemm_w8a8_gated(
+            A.data_ptr(), _operand(Wg, torch.int8, (F, K), "Wg", dev),
+            _operand(Wu, torch.int8, (F, K), "Wu", dev),
+            _operand(a_scales, torch.float32, (M,), "a_scales", dev),
+            _operand(g_scales, torch.float32, (F,), "g_scales", dev),
+            _operand(u_scales, torch.float32, (F,), "u_scales", dev),
+            _operand(H, out_dtype, (M, F), "H", dev), M, F, K, code, dt, handle)
+    _check(st, "qgemm_w8a8_gated")
+    return H
+
+
+def qgemm_dense_gated(X, Wg, Wu, H=None, G=None, U=None, act: str = "silu",
+                      save_preact: bool = False, stream=None):
+    """X [M,K]; Wg, Wu [F,K], all fp16 or all bf16 -> H [M,F] = act(X Wg^T) * (X Wu^T). With
+    save_preact, or with G and U given, returns (H, G, U): the pre-activations that
+    qgemm_dense_gated_backward reads. act: silu, gelu or gelu_tanh."""
+    torch = _torch()
+    dt, code = _half_type(X, "X"), _activation(act)
+    _need(X, X.dtype, 2, "X")
+    _need(Wg, X.dtype, 2, "Wg")
+    (M, K), F, dev, dtype = X.shape, Wg.shape[0], X.device, X.dtype
+    if (G is None) != (U is None):
+        raise ValueError("G and U go together")
+    save = save_preact or G is not None
+    scope, handle = _on(dev, stream)
+    with scope:
+        if H is None:
+            H = torch.empty((M, F), dtype=dtype, device=dev)
+        if save and G is None:
+            G, U = (torch.empty((M, F), dtype=dtype, device=dev) for _ in range(2))
+        st = lib().qgemm_dense_gated(
+            X.data_ptr(), _operand(Wg, dtype, (F, K), "Wg", dev),
+            _operand(Wu, dtype, (F, K), "Wu", dev), _operand(H, dtype, (M, F), "H", dev),
+            _operand(G, dtype, (M, F), "G", dev) if save else None,
+            _operand(U, dtype, (M, F), "U", dev) if save else None, M, F, K, code, dt, handle)
+    _check(st, "qgemm_dense_gated")
+    return (H, G, U) if save else H
+
+
+def qgemm_dense_gated_backward_workspace_bytes(M: int, F: int, K: int) -> int:
+    return int(lib().qgemm_dense_gated_backward_workspace_bytes(M, F, K))
+
+
+def qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U, act: str = "silu", dX=None, dWg=None,
+                               dWu=None, need_dx: bool = True, need_dw: bool = True,
+                               workspace=None, stream=None):
+    """Gradients of qgemm_dense_gated: dH, G, U [M,F], X [M,K], Wg, Wu [F,K] -> (dX [M,K], dWg,
+    dWu [F,K]), all of one type; dX is None without need_dx, dWg and dWu without need_dw.
+    workspace: a uint8 CUDA tensor of qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes
+    or more (allocated here when not given)."""
+    torch = _torch()
+    dt, code = _half_type(X, "X"), _activation(act)
+    _need(X, X.dtype, 2, "X")
+    _need(Wg, X.dtype, 2, "Wg")
+    (M, K), F, dev, dtype = X.shape, Wg.shape[0], X.device, X.dtype
+    scope, handle = _on(dev, stream)
+    with scope:
+        if need_dx and dX is None:
+            dX = torch.empty((M, K), dtype=dtype, device=dev)
+        if need_dw and dWg is None:
+            dWg = torch.empty((F, K), dtype=dtype, device=dev)
+        if need_dw and dWu is None:
+            dWu = torch.empty((F, K), dtype=dtype, device=dev)
+        if workspace is None:
+            need = qgemm_dense_gated_backward_workspace_bytes(M, F, K)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _need(workspace, torch.uint8, 1, "workspace")
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
+        st = lib().qgemm_dense_gated_backward(
+            _operand(dH, dtype, (M, F), "dH", dev), X.data_ptr(),
+            _operand(Wg, dtype, (F, K), "Wg", dev), _operand(Wu, dtype, (F, K), "Wu", dev),
+            _operand(G, dtype, (M, F), "G", dev), _operand(U, dtype, (M, F), "U", dev),
+            _operand(dX, dtype, (M, K), "dX", dev) if need_dx else None,
+            _operand(dWg, dtype, (F, K), "dWg", dev) if need_dw else None,
+            _operand(dWu, dtype, (F, K), "dWu", dev) if need_dw else None,
+            M, F, K, code, dt, workspace.data_ptr(), workspace.numel(), handle)
+    _check(st, "qgemm_dense_gated_backward")
+    return dX if need_dx else None, dWg if need_dw else None, dWu if need_dw else None
 
 
 # ---- configuration -------------------------------------------------------------------------------

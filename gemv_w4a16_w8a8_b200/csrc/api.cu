@@ -674,6 +674,16 @@ bool page_locked(const void *p)
     return a.type == cudaMemoryTypeHost;
 }
 } // namespace
+
+qg_status current_device(int *sms, unsigned int **err_word)
+{
+    DeviceInfo *d = nullptr;
+    const qg_status s = probe_device(&d);
+    if (s != QG_OK) return s;
+    *sms = d->sms;
+    *err_word = d->err_word;
+    return QG_OK;
+}
 } // namespace qg
 
 using namespace qg;

@@ -85,6 +85,9 @@ int tc_max_stages(const Problem &p, int bn);
 // Number of upcast-weight buffers the tensor-core kernel keeps for this ring depth (0: none).
 int tc_dq_buffers(const Problem &p, int bn, int stages);
 
+// The current device's multiprocessor count and error word (QG_ERR_NOT_SM100 off a B200).
+qg_status current_device(int *sms, unsigned int **err_word);
+
 // ------------------------------------------------------------------------------------------
 // PTX wrappers
 // ------------------------------------------------------------------------------------------

@@ -70,6 +70,19 @@ typedef enum qg_op {
     QG_OP_W2A8_INTERLEAVED = 5    /* W2A8 with weights from quant_pack_int2_interleaved  */
 } qg_op;
 
+/* Type of 16-bit activations, outputs and gradients in the entry points that take `dtype`. */
+typedef enum qg_dtype {
+    QG_F16 = 0,   /* IEEE binary16 */
+    QG_BF16 = 1   /* bfloat16      */
+} qg_dtype;
+
+/* Activation of the gated feed-forward block, evaluated in fp32. */
+typedef enum qg_act {
+    QG_ACT_SILU = 0,      /* g / (1 + exp(-g))                                             */
+    QG_ACT_GELU = 1,      /* g * Phi(g), Phi the normal distribution function              */
+    QG_ACT_GELU_TANH = 2  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))               */
+} qg_act;
+
 typedef enum qg_path {
     QG_PATH_AUTO = 0, /* let the library choose                                               */
     QG_PATH_GEMV = 1, /* small-M streaming kernels (weights read once with 128-bit loads)      */
@@ -270,6 +283,78 @@ qg_status qgemm_w2a8_interleaved(const int8_t *A, const uint32_t *Wq, int32_t *C
  */
 qg_status qgemm_dense_f16(const void *A, const void *W, void *C, int M, int N, int K,
                           int split_k, cudaStream_t stream);
+
+/* ---- 8-bit activations with scales; the gated feed-forward block ------------------------------ */
+
+/*
+ * Quantise 16-bit activations to int8 with one scale a token. X: fp16 / bf16 [M, K] (dtype).
+ * Q: int8 [M, K]; scales: fp32 [M]. Per row, every step a binary32 operation rounded to nearest:
+ *     amax = max_k |x|,  s = amax / 127 (1 for a row of zeros),  q = rint(x * (127 / amax)),
+ * rint half to even, so -127 <= q <= 127 and |x - q s| <= s / 2 up to those roundings. A row with
+ * amax < 2^-60 (bf16 only) forms q from x and amax times 2^64, which is exact. A row that holds
+ * an infinity or a NaN gets scale NaN and codes 0: what is computed from it is NaN.
+ * Requires K % 8 == 0; X and Q 16-byte aligned, scales 4-byte aligned.
+ */
+qg_status quant_int8_tokens(const void *X, int8_t *Q, float *scales, int M, int K, int dtype,
+                            cudaStream_t stream);
+
+/*
+ * W8A8 with a scale for each token and each output channel, 16-bit output. A: int8 [M, K];
+ * W: int8 [N, K]; a_scales: fp32 [M]; w_scales: fp32 [N]; bias: `dtype` [N] or NULL.
+ *     C[m, n] = a_scales[m] * w_scales[n] * sum_k A[m, k] W[n, k] (+ bias[n])
+ * The sum is exact in int32; its conversion, the two products (a_scales first) and the bias's
+ * addition are binary32 operations; one rounding to `dtype` at the end. Any int8 value is
+ * allowed. The result is the same bit for bit from run to run.
+ * Requires K % 16 == 0, K < 131072 (above it the sum could leave int32); A, W, C 16-byte
+ * aligned, scales 4-byte, bias 2-byte aligned.
+ */
+qg_status qgemm_w8a8_scaled(const int8_t *A, const int8_t *W, const float *a_scales,
+                            const float *w_scales, const void *bias, void *C, int M, int N, int K,
+                            int dtype, cudaStream_t stream);
+
+/*
+ * The gated feed-forward block's first half on int8 operands, in one kernel: A: int8 [M, K];
+ * Wg, Wu: int8 [F, K]; a_scales: fp32 [M]; g_scales, u_scales: fp32 [F]; H: `dtype` [M, F].
+ *     g = a_scales[m] g_scales[f] sum_k A Wg,   u = a_scales[m] u_scales[f] sum_k A Wu,
+ *     H[m, f] = act(g) * u                      (act: qg_act; fp32, rounded once)
+ * Requirements and reproducibility as qgemm_w8a8_scaled, with F for N.
+ */
+qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
+                           const float *a_scales, const float *g_scales, const float *u_scales,
+                           void *H, int M, int F, int K, int act, int dtype, cudaStream_t stream);
+
+/*
+ * The same on 16-bit operands (all of type `dtype`), sums in fp32: X [M, K]; Wg, Wu [F, K];
+ *     G = X Wg^T,  U = X Wu^T,  H = act(G) * U     [M, F]
+ * G and U: NULL, or both given for training: they receive the pre-activations, rounded to
+ * `dtype`, that qgemm_dense_gated_backward reads (H is formed from the unrounded ones).
+ * Requires K % 8 == 0; every pointer 16-byte aligned. The result is the same bit for bit from
+ * run to run.
+ */
+qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void *H, void *G,
+                            void *U, int M, int F, int K, int act, int dtype,
+                            cudaStream_t stream);
+
+/*
+ * Gradients of qgemm_dense_gated. dH: [M, F]; X, Wg, Wu as in the forward pass; G, U: what it
+ * saved. dX: [M, K]; dWg, dWu: [F, K]; everything of type `dtype`.
+ *     dG = dH * U * act'(G),  dU = dH * act(G)             (fp32, rounded to `dtype`)
+ *     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X      (fp32 sums, rounded once)
+ * dX may be NULL, and so may dWg and dWu together; what is NULL is not computed.
+ * workspace: caller-owned device memory, 256-byte aligned, at least
+ * qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes, contents on entry and after the
+ * call of no meaning. Calls that share a workspace must not overlap on the GPU. Outputs must
+ * not overlap inputs. Requires K % 8 == 0; every pointer 16-byte aligned. The result is the
+ * same bit for bit from run to run.
+ */
+qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
+                                     const void *G, const void *U, void *dX, void *dWg, void *dWu,
+                                     int M, int F, int K, int act, int dtype, void *workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes qgemm_dense_gated_backward needs (0 if the sizes are invalid): dG and dU with
+ * rows padded to 16 bytes, and fp32 partial sums where a product's reduction is split. */
+size_t qgemm_dense_gated_backward_workspace_bytes(int M, int F, int K);
 
 /* ---- weight packing ------------------------------------------------------------------------ */
 
