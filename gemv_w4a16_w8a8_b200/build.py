@@ -11,6 +11,7 @@ from __future__ import annotations
 import argparse
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
-HEADERS = [os.path.join(ROOT, "include", "qgemm.h")] + glob.glob(os.path.join(CSRC, "*.cuh"))
+INCLUDES = (CSRC, os.path.join(ROOT, "include"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -35,6 +36,19 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _headers(src: str, seen: set | None = None) -> set:
+    """The project's own headers that a source includes, directly or through others."""
+    seen = set() if seen is None else seen
+    with open(src) as f:
+        for name in re.findall(r'^\s*#include "([^"]+)"', f.read(), flags=re.M):
+            for d in INCLUDES:
+                path = os.path.join(d, name)
+                if os.path.exists(path) and path not in seen:
+                    seen.add(path)
+                    _headers(path, seen)
+    return seen
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -44,7 +58,7 @@ def _stale(target: str, deps) -> bool:
 
 def _compile(src: str, force: bool) -> tuple[str, str]:
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-    if not force and not _stale(obj, [src] + HEADERS):
+    if not force and not _stale(obj, [src, *_headers(src)]):
         return obj, ""
     cmd = [nvcc()] + ARCH + FLAGS + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)

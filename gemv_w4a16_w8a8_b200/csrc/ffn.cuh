@@ -93,6 +93,9 @@ template <int ACT> __device__ __forceinline__ void act_both(float g, float &valu
 }
 
 // Run f with the activation and 16-bit type as template arguments.
+template <int V> struct Const {
+    static constexpr int value = V;
+};
 #define QG_DISPATCH_16(dtype, T, ...)                                                              \
     do {                                                                                           \
         if ((dtype) == QG_BF16) { using T = __nv_bfloat16; __VA_ARGS__; }                          \
@@ -133,6 +136,11 @@ cudaError_t launch_w8a8_scaled(const ScaledProblem &p, int sms, unsigned int *er
                                cudaStream_t stream);
 cudaError_t launch_dense_gated(const GatedProblem &p, int sms, unsigned int *err,
                                cudaStream_t stream);
+// Large tiles (ffn_tile.cu), any sizes: built for more than 128 tokens.
+cudaError_t launch_tile_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_tile_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_tile_dx(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_tile_dw(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err,
                                   cudaStream_t stream);
 

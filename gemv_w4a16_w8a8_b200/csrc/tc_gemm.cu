@@ -60,18 +60,6 @@ template <bool TOKA> constexpr int wrows() { return TOKA ? kRowsT : kRowsW; }
 constexpr int kSlabBytes = 128;        // bytes of K per stage and row (64 fp16 / 128 int8)
 constexpr int kGroupT = 8;             // token tiles per raster group
 
-// Shared-memory matrix descriptor: K-major, SWIZZLE_128B, 8-row core groups 1024 B apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
-{
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFF);          // start address
-    d |= (uint64_t)1 << 16;                          // leading byte offset (unused here)
-    d |= (uint64_t)(1024 >> 4) << 32;                // stride byte offset: next 8 rows
-    d |= (uint64_t)1 << 46;                          // descriptor version
-    d |= (uint64_t)2 << 61;                          // swizzle: 128B
-    return d;
-}
-
 template <int MODE>
 __device__ __forceinline__ void mma_issue(uint32_t dtm, uint64_t a, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate)
@@ -87,12 +75,6 @@ __device__ __forceinline__ void mma_issue(uint32_t dtm, uint64_t a, uint64_t b, 
                      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                      : "memory");
     }
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
 }
 
 // ---- CTA pairs (cta_group::2): one MMA spans the tensor cores of two SMs of a cluster --------
@@ -115,73 +97,6 @@ __device__ __forceinline__ void mma_issue_pair(uint32_t dtm, uint64_t a, uint64_
                      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
                      : "memory");
     }
-}
-
-// arrive on the barrier at the same offset in both CTAs of the pair once the MMAs finish
-__device__ __forceinline__ void mma_commit_pair_both(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::"
-                 "cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
-                 : "memory");
-}
-
-// arrive on this CTA's own barrier once the MMAs finish
-__device__ __forceinline__ void mma_commit_pair_local(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// address of the same shared-memory location in CTA `rank` of this cluster
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
-
-// arrival (release at cluster scope) on a barrier given by its shared::cluster address
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-                 : "memory");
-}
-
-// every thread of both CTAs
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-
-// 2-D TMA load into this CTA's shared memory that completes its bytes on a barrier of either
-// CTA of the pair (given by its shared::cluster address); no multicast
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map,
-                                                 uint32_t bar_cluster, int x, int y)
-{
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx"
-                 "::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar_cluster)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                   "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
-                   "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // Instruction descriptor: dense, K-major A and B, M = MR (128, or 256 for a CTA pair), N = BN.
