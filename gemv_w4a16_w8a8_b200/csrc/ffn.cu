@@ -8,6 +8,7 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFewTokens = 128;        // up to here the weights' stream is the bound
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32); rows of Fp elements. Bound: HBM, 10 bytes an element.
@@ -30,11 +31,13 @@ grad_act_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__re
 
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream)
 {
+    if (p.M <= kFewTokens) return launch_small_scaled(p, sms, err, stream);
     return launch_tile_scaled(p, sms, err, stream);
 }
 
 cudaError_t launch_dense_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream)
 {
+    if (p.M <= kFewTokens) return launch_small_gated(p, sms, err, stream);
     return launch_tile_gated(p, sms, err, stream);
 }
 
@@ -48,7 +51,8 @@ cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err
         });
     });
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && p.dX) e = launch_tile_dx(p, sms, err, stream);
+    if (e == cudaSuccess && p.dX)
+        e = p.M <= kFewTokens ? launch_small_dx(p, sms, err, stream) : launch_tile_dx(p, sms, err, stream);
     if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, sms, err, stream);
     return e;
 }

@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace qg {
@@ -141,6 +143,10 @@ cudaError_t launch_tile_scaled(const ScaledProblem &p, int sms, unsigned int *er
 cudaError_t launch_tile_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_dx(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_dw(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream);
+// Few tokens (ffn_small.cu), any sizes: built for up to 128 tokens.
+cudaError_t launch_small_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_small_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_small_dx(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err,
                                   cudaStream_t stream);
 

@@ -117,7 +117,7 @@ __device__ __forceinline__ void mma_pair(uint32_t dtm, uint64_t a, uint64_t b, u
 // (1) operands; bits 15 and 16: MN-major A and B.
 template <bool I8, typename T, int BN, bool AMN, bool BMN> constexpr uint32_t instr_desc()
 {
-    const uint32_t in = I8 ? 1u : (sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1u : 0u);
+    const uint32_t in = I8 ? 1u : (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
     return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (AMN ? 1u : 0u) << 15 | (BMN ? 1u : 0u) << 16 |
            (uint32_t)(BN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
 }
@@ -452,7 +452,7 @@ struct Matrix {          // a 16-bit or int8 matrix [rows, cols] with `pitch` by
 template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, bool mn, int box_rows)
 {
     const CUtensorMapDataType dt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                      : (__is_same(T, __nv_bfloat16) ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : (std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
     return make_map(m, dt, x.p, x.cols, x.rows, x.pitch, I8 ? 128 : 64, mn ? 64 : box_rows,
                     CU_TENSOR_MAP_SWIZZLE_128B);

@@ -170,6 +170,13 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+
 // address of the same shared-memory location in CTA `rank` of this cluster
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank)
 {
