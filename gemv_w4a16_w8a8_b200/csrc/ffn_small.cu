@@ -360,9 +360,11 @@ cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, cons
     // weights: 128 rows, 64 of each for kGated, 64 rows of the reduction for kDx
     CUtensorMap tw0, tw1, tx0, tx1;
     const int wbox = FORM == kScaled ? 128 : 64;
-    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tw1, w1, wbox) || !map_of<I8, T>(&tx0, x0, BN) ||
-        !map_of<I8, T>(&tx1, x1, BN))
-        return cudaErrorInvalidValue;
+    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tx0, x0, BN)) return cudaErrorInvalidValue;
+    tw1 = tw0;
+    tx1 = tx0;
+    if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
+    if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, BN)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.blockDim = dim3(kThreads);

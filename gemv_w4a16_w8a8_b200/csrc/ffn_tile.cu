@@ -124,7 +124,7 @@ template <bool I8, typename T, int BN, bool AMN, bool BMN> constexpr uint32_t in
 
 // A warp's 32 rows x 128 bytes of results, staged in shared memory (16-byte piece j of row r at
 // j ^ (r & 7): neither side has bank conflicts) and written as whole rows: 16 bytes a lane where
-// rows of the result are 16-byte aligned, else element by element, a row at a time.
+// rows of the result are 16-byte aligned, else a row at a time, an element a lane.
 __device__ __forceinline__ void stage_put(uint8_t *stage, int lane, int j, const uint4 &v)
 {
     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
@@ -146,10 +146,11 @@ __device__ __forceinline__ void stage_flush(const uint8_t *stage, E *c, size_t l
                 *reinterpret_cast<uint4 *>(c + (size_t)r * ld + j * kPer) = v;
         }
     } else {
-        for (int r = 0; r < rows; ++r)
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r)
 #pragma unroll
             for (int q = lane; q < kCols; q += 32)
-                if (q < cols)
+                if (r < rows && q < cols)
                     c[(size_t)r * ld + q] = *reinterpret_cast<const E *>(
                         stage + r * 128 + (((q / kPer) ^ (r & 7)) << 4) + (q % kPer) * sizeof(E));
     }
@@ -413,7 +414,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 #pragma unroll
                             for (int q = 0; q < 8; ++q)
                                 stage_put(stage, lane, q, make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]));
-                            stage_flush(stage, dst + w.n0 + c, N, rows, cols, lane, vec);
+                            if (vec || (N & 1))
+                                stage_flush(stage, dst + w.n0 + c, N, rows, cols, lane, vec);
+                            else     // pairs of elements
+                                stage_flush(stage, reinterpret_cast<uint32_t *>(dst + w.n0 + c), N / 2, rows,
+                                            cols / 2, lane, false);
                         };
                         write(hw, c0);
                         if constexpr (FORM == kGated && !I8) {
@@ -496,9 +501,11 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
         pairs = pairs_of[dev];
     }
     CUtensorMap ta0, ta1, tb0, tb1;
-    if (!map_of<I8, T>(&ta0, a0, AMN, kRows) || !map_of<I8, T>(&ta1, a1, AMN, kRows) ||
-        !map_of<I8, T>(&tb0, b0, BMN, BN / 2) || !map_of<I8, T>(&tb1, b1, BMN, BN / 2))
-        return cudaErrorInvalidValue;
+    if (!map_of<I8, T>(&ta0, a0, AMN, kRows) || !map_of<I8, T>(&tb0, b0, BMN, BN / 2)) return cudaErrorInvalidValue;
+    ta1 = ta0;
+    tb1 = tb0;
+    if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, AMN, kRows)) return cudaErrorInvalidValue;
+    if (b1.p != b0.p && !map_of<I8, T>(&tb1, b1, BMN, BN / 2)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(2 * std::min(shape.units, pairs));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta0, ta1, tb0, tb1, shape, out, err);
     return e != cudaSuccess ? e : cudaGetLastError();
