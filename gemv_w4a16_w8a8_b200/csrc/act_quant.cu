@@ -58,6 +58,8 @@ quant_tokens_kernel(const T *__restrict__ X, int8_t *__restrict__ Q, float *__re
     const uint4 *x = reinterpret_cast<const uint4 *>(X + (live ? row : 0) * K);
     uint2 *q = reinterpret_cast<uint2 *>(Q + (live ? row : 0) * K);
     const int n = live ? K / 8 : 0;
+    grid_release();
+    grid_wait();
 
     uint4 v[kVec];
     uint32_t top = 0;
@@ -97,9 +99,8 @@ template <typename T, int TPR, bool LONG>
 cudaError_t run(const void *X, int8_t *Q, float *scales, int M, int K, cudaStream_t stream)
 {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR;
-    quant_tokens_kernel<T, TPR, LONG><<<(unsigned)((M + (long long)kRows - 1) / kRows), kThreads, 0, stream>>>(
-        static_cast<const T *>(X), Q, scales, M, K);
-    return cudaGetLastError();
+    return launch_dependent(quant_tokens_kernel<T, TPR, LONG>, dim3((unsigned)((M + (long long)kRows - 1) / kRows)),
+                            dim3(kThreads), 0, 1, stream, static_cast<const T *>(X), Q, scales, M, K);
 }
 
 } // namespace

@@ -11,20 +11,56 @@ constexpr int kThreads = 256;
 constexpr int kFewTokens = 128;        // up to here the weights' stream is the bound
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
-// read them sum in fp32); rows of Fp elements. Bound: HBM, 10 bytes an element.
+// read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
+// elements. Bound: HBM, 10 bytes an element: eight elements a thread by 16-byte loads and stores
+// where F % 8 == 0 (VEC); otherwise one by one.
 template <typename T, int ACT>
+__device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, uint32_t &dg, uint32_t &du)
+{
+    const float2 h2 = unpack2<T>(dh), g2 = unpack2<T>(g), u2 = unpack2<T>(u);
+    float v0, d0, v1, d1;
+    act_both<ACT>(g2.x, v0, d0);
+    act_both<ACT>(g2.y, v1, d1);
+    dg = pack2<T>(h2.x * u2.x * d0, h2.y * u2.y * d1);
+    du = pack2<T>(h2.x * v0, h2.y * v1);
+}
+
+template <typename T, int ACT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 grad_act_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__restrict__ U,
-                T *__restrict__ dG, T *__restrict__ dU, int F, int Fp)
+                T *__restrict__ dG, T *__restrict__ dU, int M, int F, int Fp)
 {
-    const size_t in = (size_t)blockIdx.x * F, out = (size_t)blockIdx.x * Fp;
-    for (int f = threadIdx.x; f < F; f += kThreads) {
+    grid_release();
+    grid_wait();
+    const size_t at = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    if constexpr (VEC) {
+        if (at >= (size_t)M * F / 8) return;
+        const uint4 h = ld_stream_v4(dH + at * 8), g = ld_stream_v4(G + at * 8), u = ld_stream_v4(U + at * 8);
+        uint4 dg, du;
+        grad_pair<T, ACT>(h.x, g.x, u.x, dg.x, du.x);
+        grad_pair<T, ACT>(h.y, g.y, u.y, dg.y, du.y);
+        grad_pair<T, ACT>(h.z, g.z, u.z, dg.z, du.z);
+        grad_pair<T, ACT>(h.w, g.w, u.w, dg.w, du.w);
+        reinterpret_cast<uint4 *>(dG)[at] = dg;      // F % 8 == 0: Fp == F
+        reinterpret_cast<uint4 *>(dU)[at] = du;
+    } else {
+        if (at >= (size_t)M * F) return;
+        const size_t m = at / F, to = m * Fp + (at - m * F);
         float v, d;
-        act_both<ACT>(to_f32(G[in + f]), v, d);
-        const float dh = to_f32(dH[in + f]);
-        dG[out + f] = from_f32<T>(dh * to_f32(U[in + f]) * d);
-        dU[out + f] = from_f32<T>(dh * v);
+        act_both<ACT>(to_f32(G[at]), v, d);
+        const float dh = to_f32(dH[at]);
+        dG[to] = from_f32<T>(dh * to_f32(U[at]) * d);
+        dU[to] = from_f32<T>(dh * v);
     }
+}
+
+template <typename T, int ACT, bool VEC> cudaError_t run_grad_act(const GatedGrad &p, cudaStream_t stream)
+{
+    const size_t n = (size_t)p.M * p.F / (VEC ? 8 : 1);
+    return launch_dependent(grad_act_kernel<T, ACT, VEC>, dim3((unsigned)((n + kThreads - 1) / kThreads)),
+                            dim3(kThreads), 0, 1, stream, static_cast<const T *>(p.dH),
+                            static_cast<const T *>(p.G), static_cast<const T *>(p.U), static_cast<T *>(p.dG),
+                            static_cast<T *>(p.dU), p.M, p.F, p.Fp);
 }
 
 } // namespace
@@ -43,14 +79,12 @@ cudaError_t launch_dense_gated(const GatedProblem &p, int sms, unsigned int *err
 
 cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream)
 {
+    cudaError_t e = cudaSuccess;
     QG_DISPATCH_16(p.dtype, T, {
         QG_DISPATCH_ACT(p.act, ACT, {
-            grad_act_kernel<T, ACT><<<p.M, kThreads, 0, stream>>>(
-                static_cast<const T *>(p.dH), static_cast<const T *>(p.G), static_cast<const T *>(p.U),
-                static_cast<T *>(p.dG), static_cast<T *>(p.dU), p.F, p.Fp);
+            e = p.F % 8 ? run_grad_act<T, ACT, false>(p, stream) : run_grad_act<T, ACT, true>(p, stream);
         });
     });
-    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.dX)
         e = p.M <= kFewTokens ? launch_small_dx(p, sms, err, stream) : launch_tile_dx(p, sms, err, stream);
     if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, sms, err, stream);

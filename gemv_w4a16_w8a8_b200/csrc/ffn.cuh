@@ -111,6 +111,42 @@ template <int V> struct Const {
     } while (0)
 
 // ------------------------------------------------------------------------------------------
+// Programmatic dependent launch. Each of these kernels lets its successor's CTAs start as soon as
+// its own have all started, and touches global memory only behind grid_wait(), which returns when
+// the kernels before it on the stream have finished and their writes are visible. So a kernel's
+// launch, barrier and tensor-memory set-up run under the end of its predecessor, and stream order
+// is kept: 1.5 to 2.5 us less a call on 10 us calls that follow one another.
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch with `cluster` CTAs a cluster (along x) and programmatic dependent launch.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, int cluster,
+                             cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------
 // Launchers: queue on `stream`, return cudaGetLastError().
 // ------------------------------------------------------------------------------------------
 struct ScaledProblem {      // int8 operands: scaled matmul (W1 null) or gated (W1 = Wu)

@@ -140,6 +140,12 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
+    if (threadIdx.x == 32) {
+        prefetch_map(&tm_w0);
+        prefetch_map(&tm_x0);
+        if (FORM != kScaled) prefetch_map(&tm_w1);
+        if (FORM == kDx) prefetch_map(&tm_x1);
+    }
     if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tmem_holder)),
@@ -151,6 +157,28 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    // The first slabs of weights go to L2 before the kernels ahead on the stream have finished: a
+    // weight that one of them still writes is written in L2, so what is read behind grid_wait() is
+    // right either way.
+    auto load_w = [&](int it, auto &&copy) {
+        const int slab = s0 + it;
+        const bool second = FORM == kDx && slab >= shape.seg_slabs;
+        const int k = (second ? slab - shape.seg_slabs : slab) * kElems;
+        if constexpr (FORM == kDx) {
+            copy(0, second ? &tm_w1 : &tm_w0, n0, k);
+            copy(8192, second ? &tm_w1 : &tm_w0, n0 + 64, k);
+        } else if constexpr (FORM == kGated) {
+            copy(0, &tm_w0, k, n0);
+            copy(8192, &tm_w1, k, n0);
+        } else {
+            copy(0, &tm_w0, k, n0);
+        }
+    };
+    if (warp == 4 && lane == 0)
+        for (int it = 0; it < min(ns, ST); ++it)
+            load_w(it, [](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
+    __syncwarp();
+    grid_wait();
 
     if (warp == 4) {
         // ---------------- TMA producer ----------------
@@ -164,20 +192,16 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
                 const int k = (second ? slab - shape.seg_slabs : slab) * kElems;
                 const uint32_t sw = smem_u32(base + s * L::stage), sx = sw + L::w_bytes;
                 mbar_expect_tx(full_bar(s), L::stage);
-                if constexpr (FORM == kDx) {
-                    const CUtensorMap *mw = second ? &tm_w1 : &tm_w0;
-                    tma_load_2d(sw, mw, full_bar(s), n0, k);
-                    tma_load_2d(sw + 8192, mw, full_bar(s), n0 + 64, k);
-                } else if constexpr (FORM == kGated) {
-                    tma_load_2d(sw, &tm_w0, full_bar(s), k, n0);
-                    tma_load_2d(sw + 8192, &tm_w1, full_bar(s), k, n0);
-                } else {
-                    tma_load_2d(sw, &tm_w0, full_bar(s), k, n0);
-                }
+                load_w(it, [&](int at, const CUtensorMap *map, int x, int y) {
+                    tma_load_2d(sw + at, map, full_bar(s), x, y);
+                });
                 tma_load_2d(sx, second ? &tm_x1 : &tm_x0, full_bar(s), k, t0);
             }
             __syncwarp();
         }
+        // every load is on its way: the next kernel may start (and fetch its weights into L2; any
+        // earlier, what it fetches is evicted again by what this kernel still streams)
+        grid_release();
         // every copy this warp started must land before the ring is reused or the CTA exits
         for (int i = max(0, it - ST); i < it; ++i) {
             int dummy_abort = 0;
@@ -238,11 +262,15 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         const int N = shape.N;
         auto total = [&](int token, int row, Acc (&r)[4]) {
             const uint32_t at = mine + (uint32_t)(token * kRows + row) * 4;
+            uint4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)          // all in flight before the first is added
+                v[p] = p < cl ? ld_cluster_v4(map_to_rank(at, p)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[e] = 0;
-            for (int p = 0; p < cl; ++p) {
-                const uint4 v = ld_cluster_v4(map_to_rank(at, p));
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (I8) r[e] += (int)x[e];
@@ -365,20 +393,8 @@ cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, cons
     tx1 = tx0;
     if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
     if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, BN)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(kThreads);
-    cfg.gridDim = dim3(tiles_n * parts, tiles_t);
-    cfg.dynamicSmemBytes = L::total;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = parts;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tw0, tw1, tx0, tx1, shape, out, err);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(kern, dim3(tiles_n * parts, tiles_t), dim3(kThreads), L::total, parts, stream,
+                            tw0, tw1, tx0, tx1, shape, out, err);
 }
 
 template <int FORM, bool I8, typename T>

@@ -212,6 +212,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    grid_wait();
 
     // The producer and MMA warps run with all lanes and issue from lane 0, so that addresses and
     // coordinates stay warp-uniform.
@@ -256,6 +257,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                 __syncwarp();
             }
         }
+        grid_release();        // every load is on its way: the next kernel may start
         // every copy this warp started must land before the CTA can exit
         if (rank == 0) {
             for (int i = max(0, it - ST); i < it; ++i) {
@@ -470,17 +472,6 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
     using L = Ring<BN>;
     constexpr bool AMN = FORM == kDw, BMN = FORM == kDx || FORM == kDw;
     auto kern = tile_kernel<FORM, I8, T, BN>;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::total;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     // per device: the shared-memory opt-in and the number of pairs that fit at once
     static std::mutex mu;
     static int pairs_of[64] = {};
@@ -491,7 +482,17 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
         if (!pairs_of[dev]) {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
             if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
             cfg.gridDim = dim3(2);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = L::total;
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
             int n = 0;
             e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
             if (e != cudaSuccess) return e;
@@ -506,9 +507,8 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
     tb1 = tb0;
     if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, AMN, kRows)) return cudaErrorInvalidValue;
     if (b1.p != b0.p && !map_of<I8, T>(&tb1, b1, BMN, BN / 2)) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(2 * std::min(shape.units, pairs));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta0, ta1, tb0, tb1, shape, out, err);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(kern, dim3(2 * std::min(shape.units, pairs)), dim3(kThreads), L::total, 2, stream,
+                            ta0, ta1, tb0, tb1, shape, out, err);
 }
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
