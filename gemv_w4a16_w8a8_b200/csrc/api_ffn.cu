@@ -61,7 +61,7 @@ qg_status qgemm_w8a8_scaled(const int8_t *A, const int8_t *W, const float *a_sca
     const qg_status s = current_device(&sms, &err);
     if (s != QG_OK) return s;
     const ScaledProblem p{A, W, nullptr, a_scales, w_scales, nullptr, bias, C, M, N, K, 0, dtype};
-    return launched(launch_w8a8_scaled(p, sms, err, stream));
+    return launched(launch_w8a8_scaled(p, err, stream));
 }
 
 qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
@@ -80,7 +80,7 @@ qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
     const qg_status s = current_device(&sms, &err);
     if (s != QG_OK) return s;
     const ScaledProblem p{A, Wg, Wu, a_scales, g_scales, u_scales, nullptr, H, M, F, K, act, dtype};
-    return launched(launch_w8a8_scaled(p, sms, err, stream));
+    return launched(launch_w8a8_scaled(p, err, stream));
 }
 
 qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void *H, void *G,
@@ -99,13 +99,13 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
     const qg_status s = current_device(&sms, &err);
     if (s != QG_OK) return s;
     const GatedProblem p{X, Wg, Wu, H, G, U, M, F, K, act, dtype};
-    return launched(launch_dense_gated(p, sms, err, stream));
+    return launched(launch_dense_gated(p, err, stream));
 }
 
 size_t qgemm_dense_gated_backward_workspace_bytes(int M, int F, int K)
 {
     if (M <= 0 || F <= 0 || K <= 0 || K % 8) return 0;
-    return 2 * grad_bytes(M, F);
+    return 2 * grad_bytes(M, F) + round256(tile_grad_part_bytes(M, F, K));
 }
 
 qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
@@ -129,8 +129,8 @@ qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *
     if (s != QG_OK) return s;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const GatedGrad p{dH, X, Wg, Wu, G, U, dX, dWg, dWu, ws, ws + grad_bytes(M, F), M, F, K, act,
-                      dtype, padded_f(F)};
-    return launched(launch_gated_backward(p, sms, err, stream));
+                      dtype, padded_f(F), reinterpret_cast<float *>(ws + 2 * grad_bytes(M, F))};
+    return launched(launch_gated_backward(p, err, stream));
 }
 
 } // extern "C"

@@ -8,7 +8,7 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewTokens = 128;        // up to here the weights' stream is the bound
+constexpr int kFewTokens = 64;         // up to here the weights' stream is the bound in every case
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
@@ -65,19 +65,24 @@ template <typename T, int ACT, bool VEC> cudaError_t run_grad_act(const GatedGra
 
 } // namespace
 
-cudaError_t launch_w8a8_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
-    if (p.M <= kFewTokens) return launch_small_scaled(p, sms, err, stream);
-    return launch_tile_scaled(p, sms, err, stream);
+    const int slabs = (p.K + 127) / 128;
+    const bool gated = p.W1 != nullptr;
+    if (p.M <= kFewTokens || small_us(p.M, p.N, gated, slabs) < tile_us(p.M, p.N, gated, true, slabs))
+        return launch_small_scaled(p, err, stream);
+    return launch_tile_scaled(p, err, stream);
 }
 
-cudaError_t launch_dense_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_dense_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
-    if (p.M <= kFewTokens) return launch_small_gated(p, sms, err, stream);
-    return launch_tile_gated(p, sms, err, stream);
+    const int slabs = (p.K + 63) / 64;
+    if (p.M <= kFewTokens || small_us(p.M, p.F, true, slabs) < tile_us(p.M, p.F, true, false, slabs))
+        return launch_small_gated(p, err, stream);
+    return launch_tile_gated(p, err, stream);
 }
 
-cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     QG_DISPATCH_16(p.dtype, T, {
@@ -85,9 +90,12 @@ cudaError_t launch_gated_backward(const GatedGrad &p, int sms, unsigned int *err
             e = p.F % 8 ? run_grad_act<T, ACT, false>(p, stream) : run_grad_act<T, ACT, true>(p, stream);
         });
     });
-    if (e == cudaSuccess && p.dX)
-        e = p.M <= kFewTokens ? launch_small_dx(p, sms, err, stream) : launch_tile_dx(p, sms, err, stream);
-    if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, sms, err, stream);
+    if (e == cudaSuccess && p.dX) {
+        const bool few = p.M <= kFewTokens ||
+                         small_us(p.M, p.K, false, 2 * ((p.F + 63) / 64)) < tile_dx_us(p.M, p.F, p.K);
+        e = few ? launch_small_dx(p, err, stream) : launch_tile_dx(p, err, stream);
+    }
+    if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, err, stream);
     return e;
 }
 

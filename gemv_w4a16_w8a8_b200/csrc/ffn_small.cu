@@ -356,35 +356,65 @@ template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, int 
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Parts of the reduction: as many CTAs as run at once (two an SM), four slabs a part at least (a
-// shorter stream does not pay for the barrier that joins the parts).
-int parts_of(long tiles, int slabs, int sms)
+// Clusters of 1, 2, 4 and 8 CTAs that run at once on the device (two CTAs an SM; larger clusters
+// leave SMs of a partly filled processing cluster idle: 296, 148, 71 and 33 on a B200).
+struct Slots {
+    int clusters[4];
+};
+
+// Parts of the reduction: the most, up to 8, with which every tile's cluster still runs at once and a
+// part keeps four slabs (a shorter stream does not pay for the barrier that joins the parts).
+int parts_of(long tiles, int slabs, const Slots &slots)
 {
     int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= 2L * sms && slabs >= parts * 2 * 4) parts *= 2;
+    for (int i = 1; i < 4; ++i)
+        if (tiles <= slots.clusters[i] && slabs >= 4 << i) parts = 1 << i;
     return parts;
+}
+
+template <typename Kern> cudaError_t slots_of(Kern kern, int smem, Slots *slots)
+{
+    for (int i = 0; i < 4; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(1 << i);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1 << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&slots->clusters[i], kern, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <int FORM, bool I8, typename T, int BN>
 cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
-                      const Shape &shape, const Out &out, int sms, unsigned int *err, cudaStream_t stream)
+                      const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
 {
     using L = Ring<BN>;
     auto kern = small_kernel<FORM, I8, T, BN>;
     static std::mutex mu;
-    static bool opted_in[64] = {};
+    static Slots slots_dev[64] = {};
+    Slots slots;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     {
         std::lock_guard<std::mutex> lk(mu);
-        if (!opted_in[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+        if (!slots_dev[dev].clusters[0]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+            if (e == cudaSuccess) e = slots_of(kern, L::total, &slots);
             if (e != cudaSuccess) return e;
-            opted_in[dev] = true;
+            slots_dev[dev] = slots;
         }
+        slots = slots_dev[dev];
     }
     const int tiles_n = ceil_div(shape.N, FORM == kGated ? 64 : 128), tiles_t = ceil_div(shape.M, BN);
-    const int parts = parts_of((long)tiles_n * tiles_t, shape.slabs, sms);
+    const int parts = parts_of((long)tiles_n * tiles_t, shape.slabs, slots);
     // weights: 128 rows, 64 of each for kGated, 64 rows of the reduction for kDx
     CUtensorMap tw0, tw1, tx0, tx1;
     const int wbox = FORM == kScaled ? 128 : 64;
@@ -399,17 +429,30 @@ cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, cons
 
 template <int FORM, bool I8, typename T>
 cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
-                         const Shape &shape, const Out &out, int sms, unsigned int *err, cudaStream_t stream)
+                         const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
 {
-    if (shape.M <= 16) return launch_bn<FORM, I8, T, 16>(w0, w1, x0, x1, shape, out, sms, err, stream);
-    if (shape.M <= 32) return launch_bn<FORM, I8, T, 32>(w0, w1, x0, x1, shape, out, sms, err, stream);
-    if (shape.M <= 64) return launch_bn<FORM, I8, T, 64>(w0, w1, x0, x1, shape, out, sms, err, stream);
-    return launch_bn<FORM, I8, T, 128>(w0, w1, x0, x1, shape, out, sms, err, stream);
+    if (shape.M <= 16) return launch_bn<FORM, I8, T, 16>(w0, w1, x0, x1, shape, out, err, stream);
+    if (shape.M <= 32) return launch_bn<FORM, I8, T, 32>(w0, w1, x0, x1, shape, out, err, stream);
+    if (shape.M <= 64) return launch_bn<FORM, I8, T, 64>(w0, w1, x0, x1, shape, out, err, stream);
+    return launch_bn<FORM, I8, T, 128>(w0, w1, x0, x1, shape, out, err, stream);
 }
 
 } // namespace
 
-cudaError_t launch_small_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+// Estimate for a B200, from the device times of 100 to 1024 tokens at 512 to 11008 columns and 2048 to
+// 11008 values of reduction: with 128 tokens a tile an SM takes a slab in 0.5 us alone and two
+// in 0.75 us (32 KB each, at what L2 delivers to an SM).
+double small_us(int M, int N, bool gated, int slabs)
+{
+    const Slots b200 = {{296, 148, 71, 33}};
+    const long tiles = (long)ceil_div(N, gated ? 64 : 128) * ceil_div(M, 128);
+    const int parts = parts_of(tiles, slabs, b200);
+    const long ctas = tiles * parts;
+    const double waves = ctas <= 296 ? 1.0 : ctas / 296.0;
+    return 5.5 + waves * ceil_div(slabs, parts) * (ctas <= 148 ? 0.5 : 0.75);
+}
+
+cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K;
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
@@ -418,12 +461,12 @@ cudaError_t launch_small_scaled(const ScaledProblem &p, int sms, unsigned int *e
     const int slabs = ceil_div(p.K, 128);
     const Shape shape{p.M, p.N, slabs, slabs, p.act};
     QG_DISPATCH_16(p.dtype, T, {
-        if (p.W1) return launch_small<kGated, true, T>(w, w1, a, a, shape, out, sms, err, stream);
-        return launch_small<kScaled, true, T>(w, w, a, a, shape, out, sms, err, stream);
+        if (p.W1) return launch_small<kGated, true, T>(w, w1, a, a, shape, out, err, stream);
+        return launch_small<kScaled, true, T>(w, w, a, a, shape, out, err, stream);
     });
 }
 
-cudaError_t launch_small_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K, pitch = K * 2;
     const Matrix x{p.X, (uint64_t)p.M, K, pitch}, g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
@@ -431,11 +474,11 @@ cudaError_t launch_small_gated(const GatedProblem &p, int sms, unsigned int *err
     const int slabs = ceil_div(p.K, 64);
     const Shape shape{p.M, p.F, slabs, slabs, p.act};
     QG_DISPATCH_16(p.dtype, T, {
-        return launch_small<kGated, false, T>(g, u, x, x, shape, out, sms, err, stream);
+        return launch_small<kGated, false, T>(g, u, x, x, shape, out, err, stream);
     });
 }
 
-cudaError_t launch_small_dx(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
@@ -444,7 +487,7 @@ cudaError_t launch_small_dx(const GatedGrad &p, int sms, unsigned int *err, cuda
     const int slabs = ceil_div(p.F, 64);
     const Shape shape{p.M, p.K, slabs, 2 * slabs, 0};
     QG_DISPATCH_16(p.dtype, T, {
-        return launch_small<kDx, false, T>(wg, wu, dg, du, shape, out, sms, err, stream);
+        return launch_small<kDx, false, T>(wg, wu, dg, du, shape, out, err, stream);
     });
 }
 

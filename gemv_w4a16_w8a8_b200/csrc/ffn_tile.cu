@@ -541,30 +541,71 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Time of a slab's four MMAs, relative to bn = 256: they run at the full rate from about 200
-// columns on and cost the same below it (the 256 x 32-byte operand is read either way): 394
-// cycles a slab at 128 columns, 512 at 256.
-double slab_cost(int bn) { return std::max(0.77, bn / 256.0); }
+// Widths that the MMA of a pair takes: multiples of 32 for int8 and of 16 for 16-bit types; for
+// MN-major operands whole chunks of 64 values in each CTA.
+constexpr int kStepI8 = 32, kStep16 = 16, kStepMn = 128;
+constexpr int kPairs = 74;             // of a B200
+constexpr int kMaxParts = 16;
 
-// Tile width with the shortest schedule: whole waves of tiles over the CTA pairs, each wave as long
-// as its MMAs. 2 x 43 tiles of 256 columns on 74 pairs, say, take two waves with the second mostly
-// idle; 2 x 58 tiles of 192 take two waves of 0.77. step: the widths that the MMA of a pair takes
-// (multiples of 32 for int8, of 16 for 16 bits) or, for MN-major operands, whole chunks of 64
-// values in each CTA.
-int tile_width(int M, int N, int results, bool gated, int step, int pairs)
+struct Plan {
+    int bn, parts;
+    double us;                         // estimate for a B200
+};
+
+// Tile width and parts of the reduction with the shortest schedule: whole waves of units over the
+// CTA pairs. A slab takes 0.34 us in a wave that fills the device, nearly whatever the width:
+// 128 columns 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and
+// L2 delivers little more than 90 GB/s to an SM); so fewest waves win, and among them the narrower
+// tile, whose epilogue is shorter. 2 x 43 tiles of 256 columns on 74 pairs, say, leave most of a second
+// wave idle: 2 x 69 tiles of 160 take the same two waves 15 % faster (509 x 11007 x 4080: 38.3 ->
+// 32.4 us). Parts cost their fp32 sums' way to memory and back and a second kernel.
+Plan plan_tiles(int M, int N, int results, bool gated, int step, int slabs, int max_parts)
 {
     const long tm = ceil_div(M, kTileM);
-    int best = kMaxBn;
-    double least = 0;
-    for (int bn = kMaxBn; bn >= 64; bn -= step) {
-        const long tiles = tm * ceil_div(N, gated ? bn / 2 : bn) * results;
-        const double t = (double)((tiles + pairs - 1) / pairs) * slab_cost(bn);
-        if (bn == kMaxBn || t < least - 1e-9) {
-            least = t;
-            best = bn;
+    Plan best{kMaxBn, 1, 1e30};
+    for (int parts = 1; parts <= max_parts; ++parts) {
+        const int part_slabs = ceil_div(slabs, parts);
+        if (parts > 1 && (part_slabs < 8 || ceil_div(slabs, part_slabs) != parts)) continue;
+        for (int bn = kMaxBn; bn >= 64; bn -= step) {
+            const long units = tm * ceil_div(N, gated ? bn / 2 : bn) * results * parts;
+            if (parts > 1 && units > kPairs) continue;
+            const double slab = 0.34 * (0.88 + 0.12 * bn / kMaxBn);
+            double us = 3.5 + (double)((units + kPairs - 1) / kPairs) * part_slabs * slab;
+            if (parts > 1) us += 2.5 + (double)results * M * N * 8 * parts / 5e6;
+            if (us < best.us - 1e-9) best = Plan{bn, parts, us};
         }
     }
     return best;
+}
+
+Plan plan_dx(int M, int F, int K) { return plan_tiles(M, K, 1, false, kStepMn, 2 * ceil_div(F, 64), kMaxParts); }
+Plan plan_dw(int M, int F, int K) { return plan_tiles(F, K, 2, false, kStepMn, ceil_div(M, 64), kMaxParts); }
+
+// Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n)
+{
+    grid_release();
+    grid_wait();
+    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (at >= n) return;
+    const float *src = part + (size_t)blockIdx.y * parts * n + at;
+    float r[8] = {};
+    for (int p = 0; p < parts; ++p, src += n) {
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        r[0] += a.x, r[1] += a.y, r[2] += a.z, r[3] += a.w;
+        r[4] += b.x, r[5] += b.y, r[6] += b.z, r[7] += b.w;
+    }
+    *reinterpret_cast<uint4 *>((blockIdx.y ? c1 : c0) + at) =
+        make_uint4(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]), pack2<T>(r[4], r[5]), pack2<T>(r[6], r[7]));
+}
+
+template <typename T>
+cudaError_t join_parts(const float *part, void *c0, void *c1, const Shape &s, cudaStream_t stream)
+{
+    const long long n = (long long)s.M * s.N;
+    return launch_dependent(join_kernel<T>, dim3((unsigned)((n / 8 + 255) / 256), c1 ? 2 : 1), dim3(256), 0, 1, stream,
+                            part, static_cast<T *>(c0), static_cast<T *>(c1), s.parts, n);
 }
 
 Shape shape_of(int M, int N, int bn, int ncol, int results, int seg_slabs, int segs, int parts, int act)
@@ -587,55 +628,76 @@ Shape shape_of(int M, int N, int bn, int ncol, int results, int seg_slabs, int s
 
 } // namespace
 
-cudaError_t launch_tile_scaled(const ScaledProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+double tile_us(int M, int N, bool gated, bool i8, int slabs)
+{
+    return plan_tiles(M, N, 1, gated, i8 ? kStepI8 : kStep16, slabs, 1).us;
+}
+
+double tile_dx_us(int M, int F, int K) { return plan_dx(M, F, K).us; }
+
+size_t tile_grad_part_bytes(int M, int F, int K)
+{
+    const Plan x = plan_dx(M, F, K), w = plan_dw(M, F, K);
+    const size_t nx = x.parts > 1 ? (size_t)x.parts * M * K : 0, nw = w.parts > 1 ? (size_t)w.parts * 2 * F * K : 0;
+    return std::max(nx, nw) * 4;
+}
+
+cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K;
+    const bool gated = p.W1 != nullptr;
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
-    const Matrix w1{p.W1 ? p.W1 : p.W, (uint64_t)p.N, K, K};
+    const Matrix w1{gated ? p.W1 : p.W, (uint64_t)p.N, K, K};
     const Out out{p.C, nullptr, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
-    const int bn = tile_width(p.M, p.N, 1, p.W1 != nullptr, 32, sms / 2);
-    const Shape shape = shape_of(p.M, p.N, bn, p.W1 ? bn / 2 : bn, 1, ceil_div(p.K, 128), 1, 1, p.act);
+    const int slabs = ceil_div(p.K, 128);
+    const int bn = plan_tiles(p.M, p.N, 1, gated, kStepI8, slabs, 1).bn;
+    const Shape shape = shape_of(p.M, p.N, bn, gated ? bn / 2 : bn, 1, slabs, 1, 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
-        if (p.W1) return launch_tile<kGated, true, T>(a, a, w, w1, shape, out, err, stream);
+        if (gated) return launch_tile<kGated, true, T>(a, a, w, w1, shape, out, err, stream);
         return launch_tile<kScaled, true, T>(a, a, w, w1, shape, out, err, stream);
     });
 }
 
-cudaError_t launch_tile_gated(const GatedProblem &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K, pitch = K * 2;
     const Matrix x{p.X, (uint64_t)p.M, K, pitch}, g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
     const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr, nullptr};
-    const int bn = tile_width(p.M, p.F, 1, true, 16, sms / 2);
-    const Shape shape = shape_of(p.M, p.F, bn, bn / 2, 1, ceil_div(p.K, 64), 1, 1, p.act);
+    const int slabs = ceil_div(p.K, 64);
+    const int bn = plan_tiles(p.M, p.F, 1, true, kStep16, slabs, 1).bn;
+    const Shape shape = shape_of(p.M, p.F, bn, bn / 2, 1, slabs, 1, 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
         return launch_tile<kGated, false, T>(x, x, g, u, shape, out, err, stream);
     });
 }
 
-cudaError_t launch_tile_dx(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_tile_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2};
-    const Out out{p.dX, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
-    const int bn = tile_width(p.M, p.K, 1, false, 128, sms / 2);
-    const Shape shape = shape_of(p.M, p.K, bn, bn, 1, ceil_div(p.F, 64), 2, 1, 0);
+    const Out out{p.dX, nullptr, nullptr, p.part, nullptr, nullptr, nullptr, nullptr};
+    const Plan plan = plan_dx(p.M, p.F, p.K);
+    const Shape shape = shape_of(p.M, p.K, plan.bn, plan.bn, 1, ceil_div(p.F, 64), 2, plan.parts, 0);
     QG_DISPATCH_16(p.dtype, T, {
-        return launch_tile<kDx, false, T>(dg, du, wg, wu, shape, out, err, stream);
+        const cudaError_t e = launch_tile<kDx, false, T>(dg, du, wg, wu, shape, out, err, stream);
+        if (e != cudaSuccess || shape.parts == 1) return e;
+        return join_parts<T>(p.part, p.dX, nullptr, shape, stream);
     });
 }
 
-cudaError_t launch_tile_dw(const GatedGrad &p, int sms, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_tile_dw(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix x{p.X, M, K, K * 2};
-    const Out out{p.dWg, p.dWu, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
-    const int bn = tile_width(p.F, p.K, 2, false, 128, sms / 2);
-    const Shape shape = shape_of(p.F, p.K, bn, bn, 2, ceil_div(p.M, 64), 1, 1, 0);
+    const Out out{p.dWg, p.dWu, nullptr, p.part, nullptr, nullptr, nullptr, nullptr};
+    const Plan plan = plan_dw(p.M, p.F, p.K);
+    const Shape shape = shape_of(p.F, p.K, plan.bn, plan.bn, 2, ceil_div(p.M, 64), 1, plan.parts, 0);
     QG_DISPATCH_16(p.dtype, T, {
-        return launch_tile<kDw, false, T>(dg, du, x, x, shape, out, err, stream);
+        const cudaError_t e = launch_tile<kDw, false, T>(dg, du, x, x, shape, out, err, stream);
+        if (e != cudaSuccess || shape.parts == 1) return e;
+        return join_parts<T>(p.part, p.dWg, p.dWu, shape, stream);
     });
 }
 
