@@ -124,8 +124,10 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cl = (int)cluster_size(), rank = (int)cluster_rank();
-    const int n0 = (int)(blockIdx.x / cl) * NROW;
-    const int t0 = (int)blockIdx.y * BN;
+    // tiles of the same weight rows are neighbours: those rows come from memory once
+    const int tile = (int)(blockIdx.x / cl), tiles_t = (shape.M + BN - 1) / BN;
+    const int n0 = tile / tiles_t * NROW;
+    const int t0 = tile % tiles_t * BN;
     // this CTA's part of the reduction
     const int s0 = (int)((long long)shape.slabs * rank / cl);
     const int ns = (int)((long long)shape.slabs * (rank + 1) / cl) - s0;
@@ -364,7 +366,7 @@ struct Slots {
 
 // Parts of the reduction: the most, up to 8, with which every tile's cluster still runs at once and a
 // part keeps four slabs (a shorter stream does not pay for the barrier that joins the parts).
-int parts_of(long tiles, int slabs, const Slots &slots)
+int parts_of(long long tiles, int slabs, const Slots &slots)
 {
     int parts = 1;
     for (int i = 1; i < 4; ++i)
@@ -414,7 +416,9 @@ cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, cons
         slots = slots_dev[dev];
     }
     const int tiles_n = ceil_div(shape.N, FORM == kGated ? 64 : 128), tiles_t = ceil_div(shape.M, BN);
-    const int parts = parts_of((long)tiles_n * tiles_t, shape.slabs, slots);
+    const long long tiles = (long long)tiles_n * tiles_t;
+    const int parts = parts_of(tiles, shape.slabs, slots);
+    if (tiles * parts > 0x7fffffffLL) return cudaErrorInvalidValue;
     // weights: 128 rows, 64 of each for kGated, 64 rows of the reduction for kDx
     CUtensorMap tw0, tw1, tx0, tx1;
     const int wbox = FORM == kScaled ? 128 : 64;
@@ -423,7 +427,7 @@ cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, cons
     tx1 = tx0;
     if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
     if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, BN)) return cudaErrorInvalidValue;
-    return launch_dependent(kern, dim3(tiles_n * parts, tiles_t), dim3(kThreads), L::total, parts, stream,
+    return launch_dependent(kern, dim3((unsigned)(tiles * parts)), dim3(kThreads), L::total, parts, stream,
                             tw0, tw1, tx0, tx1, shape, out, err);
 }
 
@@ -445,9 +449,9 @@ cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, c
 double small_us(int M, int N, bool gated, int slabs)
 {
     const Slots b200 = {{296, 148, 71, 33}};
-    const long tiles = (long)ceil_div(N, gated ? 64 : 128) * ceil_div(M, 128);
+    const long long tiles = (long long)ceil_div(N, gated ? 64 : 128) * ceil_div(M, 128);
     const int parts = parts_of(tiles, slabs, b200);
-    const long ctas = tiles * parts;
+    const long long ctas = tiles * parts;
     const double waves = ctas <= 296 ? 1.0 : ctas / 296.0;
     return 5.5 + waves * ceil_div(slabs, parts) * (ctas <= 148 ? 0.5 : 0.75);
 }
