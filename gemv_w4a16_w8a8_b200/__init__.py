@@ -21,7 +21,6 @@ An 8-bit gated feed-forward block from 16-bit activations X, and its 16-bit form
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -444,31 +443,40 @@ def quant_pack_int2_interleaved(vals, out=None, stream=None):
 
 # ---- 8-bit activations with scales; the gated feed-forward block ---------------------------------
 
-def _operand(t, dtype, shape, name, device):
-    """As _need, with the whole shape and the device given."""
+# A decode step makes several of these calls a layer, each a few microseconds on the device, so the
+# checks below are as few attribute reads as they can be: about 0.3 us a tensor.
+
+def _operand(t, dtype, shape, name, index):
+    """The address of a contiguous tensor of this type and shape on CUDA device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _half_type(t, name):
-    """qg_dtype of a tensor, or of a torch.dtype."""
-    torch = _torch()
-    dtype = getattr(t, "dtype", t)
-    if dtype == torch.float16:
-        return DTYPE_F16
-    if dtype == torch.bfloat16:
-        return DTYPE_BF16
-    raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
+_HALF_TYPES = None
+
+
+def _half_type(dtype, name):
+    """qg_dtype of a torch.dtype."""
+    global _HALF_TYPES
+    if _HALF_TYPES is None:
+        torch = _torch()
+        _HALF_TYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
+    if dtype not in _HALF_TYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
+    return _HALF_TYPES[dtype]
 
 
 def _activation(act):
@@ -477,43 +485,46 @@ def _activation(act):
     return ACTIVATIONS[act]
 
 
-_HERE = contextlib.nullcontext()
+def _elsewhere(t, stream):
+    """Whether a call on tensor t is for another stream, or another device, than the current one."""
+    return stream is not None or t.get_device() != _torch()._C._cuda_getDevice()
 
 
-def _on(device, stream):
-    """(context, stream handle) of a call on `device`: inside the context it is the current
-    device and `stream` its current stream, so that what the call allocates belongs to the
-    stream that writes it."""
+def _scope(t, stream):
+    """The context in which `stream` and t's device are the current ones, so that what a call
+    allocates belongs to the stream that writes it."""
     torch = _torch()
     if stream is None:
-        # the handle without a Stream object around it: 2 us less a call
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-        if device.index == torch.cuda.current_device():
-            return _HERE, handle
-        return torch.cuda.device(device), handle
+        return torch.cuda.device(t.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _current(index):
+    """Handle of the device's current stream (2 us cheaper than the Stream object around it)."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def quant_int8_tokens(X, Q=None, scales=None, stream=None):
     """X fp16/bf16 [M,K] -> (Q int8 [M,K], scales fp32 [M]): amax = max |x| of the token,
     scale = amax / 127, code = rint(x * (127 / amax)) (rule in include/qgemm.h)."""
     torch = _torch()
-    dt = _half_type(X, "X")
+    dt = _half_type(getattr(X, "dtype", None), "X")
     _need(X, X.dtype, 2, "X")
-    M, K = X.shape
-    scope, handle = _on(X.device, stream)
-    with scope:
-        if Q is None:
-            Q = torch.empty((M, K), dtype=torch.int8, device=X.device)
-        if scales is None:
-            scales = torch.empty((M,), dtype=torch.float32, device=X.device)
-        st = lib().quant_int8_tokens(X.data_ptr(), _operand(Q, torch.int8, (M, K), "Q", X.device),
-                                     _operand(scales, torch.float32, (M,), "scales", X.device),
-                                     M, K, dt, handle)
+    if _elsewhere(X, stream):
+        with _scope(X, stream):
+            return quant_int8_tokens(X, Q, scales)
+    (M, K), dev = X.shape, X.get_device()
+    if Q is None:
+        Q = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    if scales is None:
+        scales = torch.empty((M,), dtype=torch.float32, device=X.device)
+    st = lib().quant_int8_tokens(X.data_ptr(), _operand(Q, torch.int8, (M, K), "Q", dev),
+                                 _operand(scales, torch.float32, (M,), "scales", dev), M, K, dt,
+                                 _current(dev))
     _check(st, "quant_int8_tokens")
     return Q, scales
 
@@ -525,20 +536,21 @@ def qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias=None, C=None, out_dtype=Non
     torch = _torch()
     _need(A, torch.int8, 2, "A")
     _need(W, torch.int8, 2, "W")
-    (M, K), N, dev = A.shape, W.shape[0], A.device
+    if _elsewhere(A, stream):
+        with _scope(A, stream):
+            return qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias, C, out_dtype)
+    (M, K), N, dev = A.shape, W.shape[0], A.get_device()
     if out_dtype is None:
         out_dtype = torch.float16 if C is None else C.dtype
     dt = _half_type(out_dtype, "out_dtype")
-    scope, handle = _on(dev, stream)
-    with scope:
-        if C is None:
-            C = torch.empty((M, N), dtype=out_dtype, device=dev)
-        st = lib().qgemm_w8a8_scaled(
-            A.data_ptr(), _operand(W, torch.int8, (N, K), "W", dev),
-            _operand(a_scales, torch.float32, (M,), "a_scales", dev),
-            _operand(w_scales, torch.float32, (N,), "w_scales", dev),
-            None if bias is None else _operand(bias, out_dtype, (N,), "bias", dev),
-            _operand(C, out_dtype, (M, N), "C", dev), M, N, K, dt, handle)
+    if C is None:
+        C = torch.empty((M, N), dtype=out_dtype, device=A.device)
+    st = lib().qgemm_w8a8_scaled(
+        A.data_ptr(), _operand(W, torch.int8, (N, K), "W", dev),
+        _operand(a_scales, torch.float32, (M,), "a_scales", dev),
+        _operand(w_scales, torch.float32, (N,), "w_scales", dev),
+        None if bias is None else _operand(bias, out_dtype, (N,), "bias", dev),
+        _operand(C, out_dtype, (M, N), "C", dev), M, N, K, dt, _current(dev))
     _check(st, "qgemm_w8a8_scaled")
     return C
 
@@ -551,21 +563,22 @@ def qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H=None, act: str =
     torch = _torch()
     _need(A, torch.int8, 2, "A")
     _need(Wg, torch.int8, 2, "Wg")
-    (M, K), F, dev = A.shape, Wg.shape[0], A.device
+    if _elsewhere(A, stream):
+        with _scope(A, stream):
+            return qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H, act, out_dtype)
+    (M, K), F, dev = A.shape, Wg.shape[0], A.get_device()
     if out_dtype is None:
         out_dtype = torch.float16 if H is None else H.dtype
     dt, code = _half_type(out_dtype, "out_dtype"), _activation(act)
-    scope, handle = _on(dev, stream)
-    with scope:
-        if H is None:
-            H = torch.empty((M, F), dtype=out_dtype, device=dev)
-        st = lib().qgemm_w8a8_gated(
-            A.data_ptr(), _operand(Wg, torch.int8, (F, K), "Wg", dev),
-            _operand(Wu, torch.int8, (F, K), "Wu", dev),
-            _operand(a_scales, torch.float32, (M,), "a_scales", dev),
-            _operand(g_scales, torch.float32, (F,), "g_scales", dev),
-            _operand(u_scales, torch.float32, (F,), "u_scales", dev),
-            _operand(H, out_dtype, (M, F), "H", dev), M, F, K, code, dt, handle)
+    if H is None:
+        H = torch.empty((M, F), dtype=out_dtype, device=A.device)
+    st = lib().qgemm_w8a8_gated(
+        A.data_ptr(), _operand(Wg, torch.int8, (F, K), "Wg", dev),
+        _operand(Wu, torch.int8, (F, K), "Wu", dev),
+        _operand(a_scales, torch.float32, (M,), "a_scales", dev),
+        _operand(g_scales, torch.float32, (F,), "g_scales", dev),
+        _operand(u_scales, torch.float32, (F,), "u_scales", dev),
+        _operand(H, out_dtype, (M, F), "H", dev), M, F, K, code, dt, _current(dev))
     _check(st, "qgemm_w8a8_gated")
     return H
 
@@ -576,24 +589,26 @@ def qgemm_dense_gated(X, Wg, Wu, H=None, G=None, U=None, act: str = "silu",
     save_preact, or with G and U given, returns (H, G, U): the pre-activations that
     qgemm_dense_gated_backward reads. act: silu, gelu or gelu_tanh."""
     torch = _torch()
-    dt, code = _half_type(X, "X"), _activation(act)
-    _need(X, X.dtype, 2, "X")
-    _need(Wg, X.dtype, 2, "Wg")
-    (M, K), F, dev, dtype = X.shape, Wg.shape[0], X.device, X.dtype
+    dtype = getattr(X, "dtype", None)
+    dt, code = _half_type(dtype, "X"), _activation(act)
+    _need(X, dtype, 2, "X")
+    _need(Wg, dtype, 2, "Wg")
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
+    if _elsewhere(X, stream):
+        with _scope(X, stream):
+            return qgemm_dense_gated(X, Wg, Wu, H, G, U, act, save_preact)
+    (M, K), F, dev = X.shape, Wg.shape[0], X.get_device()
     save = save_preact or G is not None
-    scope, handle = _on(dev, stream)
-    with scope:
-        if H is None:
-            H = torch.empty((M, F), dtype=dtype, device=dev)
-        if save and G is None:
-            G, U = (torch.empty((M, F), dtype=dtype, device=dev) for _ in range(2))
-        st = lib().qgemm_dense_gated(
-            X.data_ptr(), _operand(Wg, dtype, (F, K), "Wg", dev),
-            _operand(Wu, dtype, (F, K), "Wu", dev), _operand(H, dtype, (M, F), "H", dev),
-            _operand(G, dtype, (M, F), "G", dev) if save else None,
-            _operand(U, dtype, (M, F), "U", dev) if save else None, M, F, K, code, dt, handle)
+    if H is None:
+        H = torch.empty((M, F), dtype=dtype, device=X.device)
+    if save and G is None:
+        G, U = (torch.empty((M, F), dtype=dtype, device=X.device) for _ in range(2))
+    st = lib().qgemm_dense_gated(
+        X.data_ptr(), _operand(Wg, dtype, (F, K), "Wg", dev),
+        _operand(Wu, dtype, (F, K), "Wu", dev), _operand(H, dtype, (M, F), "H", dev),
+        _operand(G, dtype, (M, F), "G", dev) if save else None,
+        _operand(U, dtype, (M, F), "U", dev) if save else None, M, F, K, code, dt, _current(dev))
     _check(st, "qgemm_dense_gated")
     return (H, G, U) if save else H
 
@@ -610,32 +625,35 @@ def qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U, act: str = "silu", dX=None, 
     workspace: a uint8 CUDA tensor of qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes
     or more (allocated here when not given)."""
     torch = _torch()
-    dt, code = _half_type(X, "X"), _activation(act)
-    _need(X, X.dtype, 2, "X")
-    _need(Wg, X.dtype, 2, "Wg")
-    (M, K), F, dev, dtype = X.shape, Wg.shape[0], X.device, X.dtype
-    scope, handle = _on(dev, stream)
-    with scope:
-        if need_dx and dX is None:
-            dX = torch.empty((M, K), dtype=dtype, device=dev)
-        if need_dw and dWg is None:
-            dWg = torch.empty((F, K), dtype=dtype, device=dev)
-        if need_dw and dWu is None:
-            dWu = torch.empty((F, K), dtype=dtype, device=dev)
-        if workspace is None:
-            need = qgemm_dense_gated_backward_workspace_bytes(M, F, K)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        _need(workspace, torch.uint8, 1, "workspace")
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-        st = lib().qgemm_dense_gated_backward(
-            _operand(dH, dtype, (M, F), "dH", dev), X.data_ptr(),
-            _operand(Wg, dtype, (F, K), "Wg", dev), _operand(Wu, dtype, (F, K), "Wu", dev),
-            _operand(G, dtype, (M, F), "G", dev), _operand(U, dtype, (M, F), "U", dev),
-            _operand(dX, dtype, (M, K), "dX", dev) if need_dx else None,
-            _operand(dWg, dtype, (F, K), "dWg", dev) if need_dw else None,
-            _operand(dWu, dtype, (F, K), "dWu", dev) if need_dw else None,
-            M, F, K, code, dt, workspace.data_ptr(), workspace.numel(), handle)
+    dtype = getattr(X, "dtype", None)
+    dt, code = _half_type(dtype, "X"), _activation(act)
+    _need(X, dtype, 2, "X")
+    _need(Wg, dtype, 2, "Wg")
+    if _elsewhere(X, stream):
+        with _scope(X, stream):
+            return qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U, act, dX, dWg, dWu, need_dx,
+                                              need_dw, workspace)
+    (M, K), F, dev = X.shape, Wg.shape[0], X.get_device()
+    if need_dx and dX is None:
+        dX = torch.empty((M, K), dtype=dtype, device=X.device)
+    if need_dw and dWg is None:
+        dWg = torch.empty((F, K), dtype=dtype, device=X.device)
+    if need_dw and dWu is None:
+        dWu = torch.empty((F, K), dtype=dtype, device=X.device)
+    if workspace is None:
+        need = qgemm_dense_gated_backward_workspace_bytes(M, F, K)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+    _need(workspace, torch.uint8, 1, "workspace")
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on CUDA device {dev}, got {workspace.device}")
+    st = lib().qgemm_dense_gated_backward(
+        _operand(dH, dtype, (M, F), "dH", dev), X.data_ptr(),
+        _operand(Wg, dtype, (F, K), "Wg", dev), _operand(Wu, dtype, (F, K), "Wu", dev),
+        _operand(G, dtype, (M, F), "G", dev), _operand(U, dtype, (M, F), "U", dev),
+        _operand(dX, dtype, (M, K), "dX", dev) if need_dx else None,
+        _operand(dWg, dtype, (F, K), "dWg", dev) if need_dw else None,
+        _operand(dWu, dtype, (F, K), "dWu", dev) if need_dw else None,
+        M, F, K, code, dt, workspace.data_ptr(), workspace.numel(), _current(dev))
     _check(st, "qgemm_dense_gated_backward")
     return dX if need_dx else None, dWg if need_dw else None, dWu if need_dw else None
 
