@@ -91,8 +91,7 @@ cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStr
         });
     });
     if (e == cudaSuccess && p.dX) {
-        const bool few = p.M <= kFewTokens ||
-                         small_us(p.M, p.K, false, 2 * ((p.F + 63) / 64)) < tile_dx_us(p.M, p.F, p.K);
+        const bool few = p.M <= kFewTokens || small_dx_us(p.M, p.F, p.K) < tile_dx_us(p.M, p.F, p.K);
         e = few ? launch_small_dx(p, err, stream) : launch_tile_dx(p, err, stream);
     }
     if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, err, stream);

@@ -188,5 +188,6 @@ cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaS
 cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
 double small_us(int M, int N, bool gated, int slabs);
+double small_dx_us(int M, int F, int K);
 
 } // namespace qg

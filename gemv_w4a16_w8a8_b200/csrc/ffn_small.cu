@@ -1,19 +1,27 @@
 // Few tokens: tensor-core kernel of the scaled W8A8 matmul, the gated forward products and dX.
 //
-// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns 128 weight rows (the
-// MMA's M side; 64 of the gate and the same 64 of up for kGated) and BN = 16 .. 128 tokens (its N
-// side): with few tokens an MMA costs the same for any N up to 128, so the weights go where a
-// whole 16 KB slab is consumed by four MMAs (about 40 B a clock, twice what HBM delivers to an
-// SM). Two CTAs share an SM, 100 KB of TMA ring each, which hides one CTA's start and end behind
-// the other's stream.
+// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns up to 128 tokens (the MMA's
+// M side; rows past the last token hold whatever follows in shared memory and reach no result) and R
+// rows of the weights (its N side; for kGated R / 2 of the gate and the same of up). R is any multiple
+// of four, so that the weights divide evenly over the SMs: 11008 gate and up columns, say, are 147
+// tiles of 76, where tiles of 64 left 24 of 148 SMs with twice the others' work. An MMA takes about 100
+// cycles for up to 128 rows of 32 bytes and 128 for 256, 40 to 64 B a clock, against the 24 B that HBM
+// delivers to an SM. The ring of 108 KB covers the memory's latency (44 GB/s x 2 us) and leaves room for
+// a second CTA: of this kernel, or of the next on the stream, which sets itself up while this one ends.
+//
+// Device time of calls that follow one another, weights not in L2: one token, 4096 x 11008 int8, 10.4 us
+// (45 MB, 4.3 TB/s); gate and up 11008 x 4096 int8, 17 us (90 MB, 5.3 TB/s); 16 tokens in 16 bits, 30.3 us
+// (181 MB, 6.0 TB/s); 32 tokens, 32000 x 4096, 23.8 us (133 MB, 5.6 TB/s); 16384 x 16384, 41 us (268 MB,
+// 6.5 TB/s). Of each about 3.5 us pass before the first slab arrives and after the last.
 //
 // Split reduction: the CTAs of a cluster (1, 2, 4 or 8) take consecutive parts of the reduction of
-// one tile, so that a small weight matrix still occupies every SM. Each leaves its partial tile
+// one tile, so that a small weight matrix still occupies the device. Each leaves its partial tile
 // in its own shared memory as [token][weight row]; after a cluster barrier every CTA adds its share of
-// the tile over the cluster (distributed shared memory, parts in order: the same bits every run),
-// applies scales, bias or activation and writes runs of weight rows of one token. No workspace, no
+// the columns over the cluster (distributed shared memory, parts in order: the same bits every run),
+// applies scales, bias or activation and writes runs of columns of one token. No workspace, no
 // atomics, one launch.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "ffn.cuh"
@@ -25,21 +33,25 @@ namespace {
 enum Form { kScaled, kGated, kDx };
 
 constexpr int kThreads = 192;          // warps 0-3 accumulator and output, 4 TMA, 5 MMA
-constexpr int kRows = 128, kSlab = 128;
+constexpr int kOutThreads = 128;
+constexpr int kTokens = 128, kSlab = 128;
+constexpr int kRingBytes = 108 * 1024;
+constexpr int kMaxStages = 16;
 
-template <int BN> struct Ring {
-    static constexpr int w_bytes = kRows * kSlab;
-    static constexpr int stage = w_bytes + BN * kSlab;
-    static constexpr int stages = BN == 16 ? 6 : (BN == 32 ? 5 : (BN == 64 ? 4 : 3));
-    static constexpr int bar_off = stages * stage;
-    static constexpr int nbars = 2 * stages + 1;
-    static constexpr int total = 1024 + bar_off + nbars * 8 + 16;
-    static_assert(BN * kRows * 4 <= bar_off, "the partial tile reuses the ring");
-    static_assert(2 * (total + 1024) <= 228 * 1024, "two CTAs an SM");
-};
+// after the ring: 8 rows that no copy fills, token scales, barriers, TMEM address and abort flag
+constexpr int kScaleOff = kRingBytes + 8 * kSlab, kBarOff = kScaleOff + kTokens * 4, kBars = 2 * kMaxStages + 1;
+constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 16;
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct Shape {
     int M, N;               // tokens; columns of the result
+    int cols;               // result columns of a tile, a multiple of 4
+    int second;             // first row of up in a slab, a multiple of 8 (kGated)
+    int rows;               // the MMA's N, a multiple of 16
+    int slab_rows;          // weight rows in a slab, a multiple of 8
+    int box_tokens;         // token rows in a slab, a multiple of 8
+    int stages;
+    int pitch;              // words a token of a partial tile: 4 x odd, no bank conflicts
     int seg_slabs, slabs;   // slabs of the reduction: of one product, of all
     int act;
 };
@@ -66,11 +78,11 @@ __device__ __forceinline__ void mma_one(uint32_t dtm, uint64_t a, uint64_t b, ui
                      : "memory");
 }
 
-template <bool I8, typename T, int BN, bool AMN> constexpr uint32_t instr_desc()
+template <bool I8, typename T, bool BMN> __device__ __forceinline__ uint32_t instr_desc(int n)
 {
-    const uint32_t in = I8 ? 1u : (std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
-    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (AMN ? 1u : 0u) << 15 | (uint32_t)(BN >> 3) << 17 |
-           (uint32_t)(kRows >> 4) << 24;
+    constexpr uint32_t in = I8 ? 1u : (std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
+    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (BMN ? 1u : 0u) << 16 | (uint32_t)(n >> 3) << 17 |
+           (uint32_t)(kTokens >> 4) << 24;
 }
 
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr)
@@ -88,8 +100,7 @@ template <typename T>
 __device__ __forceinline__ void store4(T *row, int n, int N, const float (&r)[4])
 {
     if ((N & 3) == 0) {
-        if (n < N)
-            *reinterpret_cast<uint2 *>(row + n) = make_uint2(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]));
+        *reinterpret_cast<uint2 *>(row + n) = make_uint2(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -97,37 +108,40 @@ __device__ __forceinline__ void store4(T *row, int n, int N, const float (&r)[4]
     }
 }
 
-template <int FORM, bool I8, typename T, int BN>
+template <int FORM, bool I8, typename T>
 __global__ void __launch_bounds__(kThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
              const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
              const Shape shape, const Out out, unsigned int *err)
 {
-    using L = Ring<BN>;
     using Acc = typename std::conditional<I8, int, float>::type;
-    constexpr bool AMN = FORM == kDx;
-    constexpr int NROW = FORM == kGated ? kRows / 2 : kRows;      // result columns of a tile
+    constexpr bool BMN = FORM == kDx;
     constexpr int kElems = I8 ? 128 : 64;
-    constexpr uint32_t kIdesc = instr_desc<I8, T, BN, AMN>();
-    constexpr uint32_t kCols = BN < 32 ? 32u : (uint32_t)BN;
-    constexpr int ST = L::stages;
+    const int ST = shape.stages, N = shape.N;
+    // (the MMA's last rows may reach past a slab: into the next one or the 8 rows behind the ring)
+    const int x_bytes = shape.box_tokens * kSlab, w_bytes = shape.slab_rows * kSlab;
+    const uint32_t cols_alloc = shape.rows <= 32 ? 32u : (shape.rows <= 64 ? 64u : (shape.rows <= 128 ? 128u : 256u));
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(base + L::bar_off);
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + L::nbars);
+    // token slabs first: the MMA reads 128 rows from the start of one, always inside the ring
+    const uint32_t ring_x = smem_u32(base), ring_w = ring_x + ST * x_bytes;
+    float *scale_s = reinterpret_cast<float *>(base + kScaleOff);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kBarOff);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     auto full_bar = [&](int s) { return smem_u32(bars + s); };
-    auto empty_bar = [&](int s) { return smem_u32(bars + ST + s); };
-    const uint32_t done_bar = smem_u32(bars + 2 * ST);
+    auto empty_bar = [&](int s) { return smem_u32(bars + kMaxStages + s); };
+    const uint32_t done_bar = smem_u32(bars + 2 * kMaxStages);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cl = (int)cluster_size(), rank = (int)cluster_rank();
+    const int cl = (int)cluster_size(), rank = (int)blockIdx.x % cl;
     // tiles of the same weight rows are neighbours: those rows come from memory once
-    const int tile = (int)(blockIdx.x / cl), tiles_t = (shape.M + BN - 1) / BN;
-    const int n0 = tile / tiles_t * NROW;
-    const int t0 = tile % tiles_t * BN;
+    const int tile = (int)blockIdx.x / cl, tiles_t = (shape.M + kTokens - 1) / kTokens;
+    const int n0 = tile / tiles_t * shape.cols;
+    const int t0 = tile % tiles_t * kTokens;
+    const int tokens = min(kTokens, shape.M - t0);
     // this CTA's part of the reduction
     const int s0 = (int)((long long)shape.slabs * rank / cl);
     const int ns = (int)((long long)shape.slabs * (rank + 1) / cl) - s0;
@@ -142,64 +156,87 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
-    if (threadIdx.x == 32) {
-        prefetch_map(&tm_w0);
-        prefetch_map(&tm_x0);
-        if (FORM != kScaled) prefetch_map(&tm_w1);
-        if (FORM == kDx) prefetch_map(&tm_x1);
-    }
     if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tmem_holder)),
-                     "r"(kCols)
+                     "r"(cols_alloc)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // The weights of slab i of this part: copy(offset in the slab, map, x, y)
+    auto weights = [&](int i, auto &&copy) {
+        const bool second = FORM == kDx && s0 + i >= shape.seg_slabs;
+        const int k = (s0 + i - (second ? shape.seg_slabs : 0)) * kElems;
+        if constexpr (FORM == kDx) {
+            for (int c = 0; c < shape.rows; c += 64) copy(c * kSlab, second ? &tm_w1 : &tm_w0, n0 + c, k);
+        } else {
+            copy(0, &tm_w0, k, n0);
+            if constexpr (FORM == kGated) copy(shape.second * kSlab, &tm_w1, k, n0);
+        }
+    };
+    // The first slabs of weights go to L2 before the kernels ahead on the stream have finished: a
+    // weight that one of them still writes is written in L2, so what is read behind grid_wait() is
+    // right either way.
+    if (warp == 4 && lane == 0) {
+        prefetch_map(&tm_x0);
+        if (FORM == kDx) prefetch_map(&tm_x1);
+        for (int i = 0; i < min(ns, ST); ++i)
+            weights(i, [](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    // The first slabs of weights go to L2 before the kernels ahead on the stream have finished: a
-    // weight that one of them still writes is written in L2, so what is read behind grid_wait() is
-    // right either way.
-    auto load_w = [&](int it, auto &&copy) {
-        const int slab = s0 + it;
-        const bool second = FORM == kDx && slab >= shape.seg_slabs;
-        const int k = (second ? slab - shape.seg_slabs : slab) * kElems;
-        if constexpr (FORM == kDx) {
-            copy(0, second ? &tm_w1 : &tm_w0, n0, k);
-            copy(8192, second ? &tm_w1 : &tm_w0, n0 + 64, k);
-        } else if constexpr (FORM == kGated) {
-            copy(0, &tm_w0, k, n0);
-            copy(8192, &tm_w1, k, n0);
-        } else {
-            copy(0, &tm_w0, k, n0);
-        }
-    };
-    if (warp == 4 && lane == 0)
-        for (int it = 0; it < min(ns, ST); ++it)
-            load_w(it, [](int, const CUtensorMap *map, int x, int y) { tma_prefetch_2d(map, x, y); });
-    __syncwarp();
     grid_wait();
+
+    // This CTA's share of the tile, in groups of four columns: some of the tokens where there are enough
+    // of them (whole rows, the longest runs), else some of the groups. A thread keeps one group, whose
+    // factors it loads now, under the weights' stream, and takes every `step`-th token.
+    const int groups = shape.cols / 4;
+    const bool by_token = tokens >= 2 * cl;
+    const int g0 = by_token ? 0 : groups * rank / cl;
+    const int ng = by_token ? groups : groups * (rank + 1) / cl - g0;
+    const int token0 = by_token ? tokens * rank / cl : 0, token1 = by_token ? tokens * (rank + 1) / cl : tokens;
+    const int step = ng > 0 ? kOutThreads / ng : 1;
+    const int n = n0 + 4 * (g0 + (ng > 0 ? (int)threadIdx.x % ng : 0));
+    const int first = token0 + (ng > 0 ? (int)threadIdx.x / ng : 0);
+    const bool mine = (int)threadIdx.x < ng * step && n < N;
+    float f0[4] = {}, f1[4] = {};
+    if (I8 && warp < 4) {
+        scale_s[threadIdx.x] = (int)threadIdx.x < tokens ? out.sa[t0 + threadIdx.x] : 0.f;
+        if (mine) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = min(n + e, N - 1);
+                f0[e] = out.sw[c];
+                if constexpr (FORM == kGated) f1[e] = out.sw1[c];
+                else if (out.bias) f1[e] = to_f32(static_cast<const T *>(out.bias)[c]);
+            }
+        }
+    }
 
     if (warp == 4) {
         // ---------------- TMA producer ----------------
-        int it = 0;
+        const uint32_t tx = (uint32_t)x_bytes + (FORM == kGated ? 2 * shape.cols : (FORM == kDx ? shape.rows : shape.cols)) * kSlab;
+        int it = 0, s = 0;
+        uint32_t phase = 1;
         for (; it < ns; ++it) {
-            const int s = it % ST;
-            if (!warp_wait(empty_bar(s), ((it / ST) & 1) ^ 1, abort_flag, err)) break;
+            const bool second = FORM == kDx && s0 + it >= shape.seg_slabs;
+            const int k = (s0 + it - (second ? shape.seg_slabs : 0)) * kElems;
+            const uint32_t xa = ring_x + s * x_bytes, wa = ring_w + s * w_bytes;
+            if (!warp_wait(empty_bar(s), phase, abort_flag, err)) break;
             if (lane == 0) {
-                const int slab = s0 + it;
-                const bool second = FORM == kDx && slab >= shape.seg_slabs;
-                const int k = (second ? slab - shape.seg_slabs : slab) * kElems;
-                const uint32_t sw = smem_u32(base + s * L::stage), sx = sw + L::w_bytes;
-                mbar_expect_tx(full_bar(s), L::stage);
-                load_w(it, [&](int at, const CUtensorMap *map, int x, int y) {
-                    tma_load_2d(sw + at, map, full_bar(s), x, y);
+                mbar_expect_tx(full_bar(s), tx);
+                weights(it, [&](int at, const CUtensorMap *map, int x, int y) {
+                    tma_load_2d(wa + at, map, full_bar(s), x, y);
                 });
-                tma_load_2d(sx, second ? &tm_x1 : &tm_x0, full_bar(s), k, t0);
+                tma_load_2d(xa, second ? &tm_x1 : &tm_x0, full_bar(s), k, t0);
             }
             __syncwarp();
+            if (++s == ST) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         // every load is on its way: the next kernel may start (and fetch its weights into L2; any
         // earlier, what it fetches is evicted again by what this kernel still streams)
@@ -211,43 +248,51 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         }
     } else if (warp == 5) {
         // ---------------- MMA issue ----------------
+        const uint32_t idesc = instr_desc<I8, T, BMN>(shape.rows);
+        int s = 0;
+        uint32_t phase = 0;
         for (int it = 0; it < ns; ++it) {
-            const int s = it % ST;
-            if (!warp_wait(full_bar(s), (it / ST) & 1, abort_flag, err)) break;
+            const uint64_t dx = sw128_desc(ring_x + s * x_bytes);
+            const uint32_t wa = ring_w + s * w_bytes;
+            const uint64_t dw = BMN ? sw128_desc_mn(wa, 8192) : sw128_desc(wa);
+            if (!warp_wait(full_bar(s), phase, abort_flag, err)) break;
             tc_fence_after();
-            const uint32_t sw = smem_u32(base + s * L::stage);
-            const uint64_t dw = AMN ? sw128_desc_mn(sw, 8192) : sw128_desc(sw);
-            const uint64_t dx = sw128_desc(sw + L::w_bytes);
-            constexpr int kw = AMN ? 128 : 2;
+            constexpr int kw = BMN ? 128 : 2;
             if (lane == 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_one<I8>(tmem_base, dw + kw * k, dx + 2 * k, kIdesc, (it | k) != 0 ? 1u : 0u);
+                    mma_one<I8>(tmem_base, dx + 2 * k, dw + kw * k, idesc, (it | k) != 0 ? 1u : 0u);
                 mma_commit(empty_bar(s));
             }
             __syncwarp();
+            if (++s == ST) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         if (lane == 0) mma_commit(done_bar);
         __syncwarp();
         int dummy_abort = 0;
         mbar_wait(done_bar, 0, &dummy_abort, nullptr);
     }
-    // The accumulator to shared memory as [token][weight row]: lane = weight row. A CTA whose waits
+    // The accumulator to shared memory as [token][weight row]: lane = token. A CTA whose waits
     // gave up has raised the error word; it goes through the same steps so that nobody hangs.
-    Acc *part = reinterpret_cast<Acc *>(base);
-    const int tokens = min(BN, shape.M - t0);
     if (warp < 4) mbar_wait(done_bar, 0, abort_flag, err);
     __syncthreads();               // the copies have landed and the MMAs have read them
-    if (warp < 4) {
+    if (warp * 32 < tokens && warp < 4) {
         tc_fence_after();
         const uint32_t tm = tmem_base + ((uint32_t)(warp * 32) << 16);
+        uint32_t *row = reinterpret_cast<uint32_t *>(base) + (size_t)threadIdx.x * shape.pitch;
+        const int used = FORM == kGated ? shape.second + shape.cols : shape.cols;
 #pragma unroll 1
-        for (int c = 0; c < tokens; c += 16) {
+        for (int c = 0; c < used; c += 16) {
             uint32_t v[16];
             tmem_ld16(tm + c, v);
+            if ((int)threadIdx.x < tokens)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                reinterpret_cast<uint32_t *>(part)[(c + q) * kRows + threadIdx.x] = v[q];
+                for (int q = 0; q < 4; ++q)
+                    if (c + 4 * q < used)
+                        *reinterpret_cast<uint4 *>(row + c + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
         tc_fence_before();
     }
@@ -255,15 +300,10 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     if (cl > 1) cluster_sync();
     else __syncthreads();
 
-    // This CTA's share of the tile: (token, 4 columns) items, tokens outermost
-    {
-        constexpr int kPer = NROW / 4;
-        const int items = tokens * kPer;
-        const int i0 = items * rank / cl, i1 = items * (rank + 1) / cl;
-        const uint32_t mine = smem_u32(part);
-        const int N = shape.N;
-        auto total = [&](int token, int row, Acc (&r)[4]) {
-            const uint32_t at = mine + (uint32_t)(token * kRows + row) * 4;
+    if (warp < 4 && mine) {
+        const uint32_t part = smem_u32(base) + (uint32_t)(n - n0) * 4;
+        auto total = [&](int token, int shift, Acc (&r)[4]) {
+            const uint32_t at = part + (uint32_t)(token * shape.pitch + shift) * 4;
             uint4 v[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p)          // all in flight before the first is added
@@ -280,29 +320,25 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
                 }
             }
         };
-        for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const int t = i / kPer, row = (i % kPer) * 4;
-            const int m = t0 + t, n = n0 + row;
-            if (n >= N) continue;
-            const size_t at = (size_t)m * N;
+        // an int32 sum scaled by its token and then its column, as the definition has it
+        auto scaled = [&](Acc x, float sa, float f) {
+            if constexpr (I8) return __fmul_rn(__fmul_rn(__int2float_rn(x), sa), f);
+            else return x;
+        };
+        for (int t = first; t < token1; t += step) {
+            const size_t at = (size_t)(t0 + t) * N;
             Acc a[4];
-            total(t, row, a);
+            total(t, 0, a);
             float r[4];
-            const float sa = I8 ? out.sa[m] : 0.f;
+            const float sa = I8 ? scale_s[t] : 0.f;
             if constexpr (FORM == kGated) {
                 Acc b[4];
-                total(t, NROW + row, b);
+                total(t, shape.second, b);
                 float g[4], u[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if constexpr (I8) {
-                        const int c = min(n + e, N - 1);
-                        g[e] = __fmul_rn(__fmul_rn(__int2float_rn(a[e]), sa), out.sw[c]);
-                        u[e] = __fmul_rn(__fmul_rn(__int2float_rn(b[e]), sa), out.sw1[c]);
-                    } else {
-                        g[e] = a[e];
-                        u[e] = b[e];
-                    }
+                    g[e] = scaled(a[e], sa, f0[e]);
+                    u[e] = scaled(b[e], sa, f1[e]);
                 }
                 QG_DISPATCH_ACT(shape.act, ACT, {
 #pragma unroll
@@ -318,12 +354,9 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    r[e] = scaled(a[e], sa, f0[e]);
                     if constexpr (I8) {
-                        const int c = min(n + e, N - 1);
-                        r[e] = __fmul_rn(__fmul_rn(__int2float_rn(a[e]), sa), out.sw[c]);
-                        if (out.bias) r[e] = __fadd_rn(r[e], to_f32(static_cast<const T *>(out.bias)[c]));
-                    } else {
-                        r[e] = a[e];
+                        if (out.bias) r[e] = __fadd_rn(r[e], f1[e]);
                     }
                 }
                 store4(static_cast<T *>(out.c0) + at, n, N, r);
@@ -336,7 +369,7 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     else __syncthreads();
     if (warp == 5) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(cols_alloc)
                      : "memory");
     }
 }
@@ -352,109 +385,137 @@ template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, int 
 {
     const CUtensorMapDataType dt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                       : (std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+                                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
     return make_map(m, dt, x.p, x.cols, x.rows, x.pitch, I8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int round_up(int a, int b) { return ceil_div(a, b) * b; }
 
-// Clusters of 1, 2, 4 and 8 CTAs that run at once on the device (two CTAs an SM; larger clusters
-// leave SMs of a partly filled processing cluster idle: 296, 148, 71 and 33 on a B200).
-struct Slots {
-    int clusters[4];
+int stages_of(int used, int box)
+{
+    return std::min(kMaxStages, kRingBytes / ((round_up(used, 8) + box) * kSlab));
+}
+
+struct Plan {
+    int cols, parts;
+    double us;                // estimate for a B200
 };
 
-// Parts of the reduction: the most, up to 8, with which every tile's cluster still runs at once and a
-// part keeps four slabs (a shorter stream does not pay for the barrier that joins the parts).
-int parts_of(long long tiles, int slabs, const Slots &slots)
-{
-    int parts = 1;
-    for (int i = 1; i < 4; ++i)
-        if (tiles <= slots.clusters[i] && slabs >= 4 << i) parts = 1 << i;
-    return parts;
-}
+// Clusters of 1, 2, 4 and 8 CTAs that run at once on a B200 with one CTA an SM (larger clusters leave SMs
+// of a partly filled processing cluster idle) and with two.
+constexpr int kClusters[2][4] = {{148, 74, 33, 15}, {296, 148, 71, 33}};
 
-template <typename Kern> cudaError_t slots_of(Kern kern, int smem, Slots *slots)
+// Columns of a tile and parts of the reduction: for every cluster size and one or two CTAs an SM, the
+// columns that divide the weights evenly over the clusters that run at once (more waves of them if a
+// tile's columns would not fit), by the estimated time of
+//   - a slab: its four MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together;
+//     more beyond 128 and 170 rows), what L2 delivers to an SM (115 GB/s), or the memory's 2 us over the
+//     slabs in flight;
+//   - the stream: the slabs of a CTA against HBM, the two slowing each other near balance;
+//   - joining: a barrier, and partial tiles through shared memory at 35 GB/s (60 GB/s unsplit).
+// Times in us of columns x parts, measured over a sweep: one token, 11008 gate and up columns, 4096 deep,
+// 76x1: 17.3, 40x1: 17.8, 64x1: 18.7, 128x1: 20.1; 16 tokens in 16 bits, 76x2: 31.1, 64x1: 33.1,
+// 76x1: 34.4; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5, 64x2: 10.6.
+Plan plan_small(int form, int M, int N, int slabs)
 {
-    for (int i = 0; i < 4; ++i) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        cfg.gridDim = dim3(1 << i);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 1 << i;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&slots->clusters[i], kern, &cfg);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
-template <int FORM, bool I8, typename T, int BN>
-cudaError_t launch_bn(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
-                      const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
-{
-    using L = Ring<BN>;
-    auto kern = small_kernel<FORM, I8, T, BN>;
-    static std::mutex mu;
-    static Slots slots_dev[64] = {};
-    Slots slots;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!slots_dev[dev].clusters[0]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
-            if (e == cudaSuccess) e = slots_of(kern, L::total, &slots);
-            if (e != cudaSuccess) return e;
-            slots_dev[dev] = slots;
+    const int tiles_t = ceil_div(M, kTokens), box = round_up(std::min(M, kTokens), 8);
+    const int halves = form == kGated ? 2 : 1;
+    const int grain = form == kDx ? 64 : 4;
+    // the MMA's 256 rows; and the partial tile fits in the ring
+    int most = 256 / halves / 8 * 8;
+    while (most > grain && (most * halves + 8) * std::min(M, kTokens) * 4 > kRingBytes) most -= 8;
+    most = std::max(grain, most / grain * grain);
+    Plan best{grain, 1, 1e30};
+    for (int per_sm = 1; per_sm <= 2; ++per_sm)
+        for (int i = 0; i < 4; ++i) {
+            const int parts = 1 << i, slots = kClusters[per_sm - 1][i];
+            if (parts > 1 && slabs < 4 * parts) break;
+            // even columns over whole waves
+            int waves = 1, cols;
+            for (;; ++waves) {
+                const long long tiles = std::max(1LL, (long long)slots * waves / tiles_t);
+                cols = round_up((int)std::min<long long>((N + tiles - 1) / tiles, N), grain);
+                if (cols <= most) break;
+                if ((long long)slots * waves > (long long)tiles_t * ceil_div(N, most)) {
+                    cols = most;
+                    break;
+                }
+            }
+            const long long ctas = (long long)ceil_div(N, cols) * tiles_t * parts;
+            const double on_sm = std::max(1.0, std::min(2.0, std::ceil(ctas / 148.0)));
+            const double rounds = std::max(1.0, ctas / ((double)kClusters[1][i] * parts));
+            const int used = form == kGated ? round_up(cols, 8) + cols : cols, tokens = std::min(M, kTokens);
+            const double mma = on_sm < 2 ? 0.29 + (used > 128 ? 0.06 : 0) : 0.40 * std::max(1.0, used / 170.0);
+            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3, 2.0 / stages_of(used, box)});
+            const double sm = ceil_div(slabs, parts) * slab * rounds;
+            const double hbm = (double)slabs * kSlab * ((double)N * halves + M) / 6.4e6;
+            const double stream = std::pow(std::pow(sm, 4) + std::pow(hbm, 4), 0.25);
+            const double tile = on_sm * tokens * used * 4.0;
+            const double join = parts > 1 ? 0.5 + 0.15 * parts + tile / 35e3 : tile / 60e3;
+            const double us = 2.5 + stream + join * rounds;
+            if (us < best.us) best = Plan{cols, parts, us};
         }
-        slots = slots_dev[dev];
-    }
-    const int tiles_n = ceil_div(shape.N, FORM == kGated ? 64 : 128), tiles_t = ceil_div(shape.M, BN);
-    const long long tiles = (long long)tiles_n * tiles_t;
-    const int parts = parts_of(tiles, shape.slabs, slots);
-    if (tiles * parts > 0x7fffffffLL) return cudaErrorInvalidValue;
-    // weights: 128 rows, 64 of each for kGated, 64 rows of the reduction for kDx
-    CUtensorMap tw0, tw1, tx0, tx1;
-    const int wbox = FORM == kScaled ? 128 : 64;
-    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tx0, x0, BN)) return cudaErrorInvalidValue;
-    tw1 = tw0;
-    tx1 = tx0;
-    if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
-    if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, BN)) return cudaErrorInvalidValue;
-    return launch_dependent(kern, dim3((unsigned)(tiles * parts)), dim3(kThreads), L::total, parts, stream,
-                            tw0, tw1, tx0, tx1, shape, out, err);
+    return best;
 }
 
 template <int FORM, bool I8, typename T>
 cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
-                         const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
+                         Shape shape, const Out &out, unsigned int *err, cudaStream_t stream)
 {
-    if (shape.M <= 16) return launch_bn<FORM, I8, T, 16>(w0, w1, x0, x1, shape, out, err, stream);
-    if (shape.M <= 32) return launch_bn<FORM, I8, T, 32>(w0, w1, x0, x1, shape, out, err, stream);
-    if (shape.M <= 64) return launch_bn<FORM, I8, T, 64>(w0, w1, x0, x1, shape, out, err, stream);
-    return launch_bn<FORM, I8, T, 128>(w0, w1, x0, x1, shape, out, err, stream);
+    auto kern = small_kernel<FORM, I8, T>;
+    static std::mutex mu;
+    static bool opted_in[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!opted_in[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            if (e != cudaSuccess) return e;
+            opted_in[dev] = true;
+        }
+    }
+    const Plan plan = plan_small(FORM, shape.M, shape.N, shape.slabs);
+    shape.cols = plan.cols;
+    shape.second = FORM == kGated ? round_up(plan.cols, 8) : 0;
+    const int used = shape.second + plan.cols;
+    shape.rows = round_up(used, 16);
+    shape.box_tokens = round_up(std::min(shape.M, kTokens), 8);
+    shape.pitch = used / 4 % 2 ? used : used + 4;
+    shape.slab_rows = round_up(used, 8);
+    shape.stages = stages_of(used, shape.box_tokens);
+    if (std::min(shape.M, kTokens) * shape.pitch * 4 > kRingBytes || shape.rows > 256 || shape.stages < 2)
+        return cudaErrorInvalidConfiguration;
+    const long long tiles = (long long)ceil_div(shape.N, plan.cols) * ceil_div(shape.M, kTokens);
+    if (tiles * plan.parts > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // a slab's box: the tile's columns of a weight matrix, or 64 rows of the reduction for kDx
+    CUtensorMap tw0, tw1, tx0, tx1;
+    const int wbox = FORM == kDx ? 64 : plan.cols;
+    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tx0, x0, shape.box_tokens)) return cudaErrorInvalidValue;
+    tw1 = tw0;
+    tx1 = tx0;
+    if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
+    if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, shape.box_tokens)) return cudaErrorInvalidValue;
+    return launch_dependent(kern, dim3((unsigned)(tiles * plan.parts)), dim3(kThreads), kSmem, plan.parts, stream,
+                            tw0, tw1, tx0, tx1, shape, out, err);
+}
+
+Shape shape_of(int M, int N, int seg_slabs, int segs, int act)
+{
+    Shape s = {};
+    s.M = M;
+    s.N = N;
+    s.seg_slabs = seg_slabs;
+    s.slabs = segs * seg_slabs;
+    s.act = act;
+    return s;
 }
 
 } // namespace
 
-// Estimate for a B200, from the device times of 100 to 1024 tokens at 512 to 11008 columns and 2048 to
-// 11008 values of reduction: with 128 tokens a tile an SM takes a slab in 0.5 us alone and two
-// in 0.75 us (32 KB each, at what L2 delivers to an SM).
-double small_us(int M, int N, bool gated, int slabs)
-{
-    const Slots b200 = {{296, 148, 71, 33}};
-    const long long tiles = (long long)ceil_div(N, gated ? 64 : 128) * ceil_div(M, 128);
-    const int parts = parts_of(tiles, slabs, b200);
-    const long long ctas = tiles * parts;
-    const double waves = ctas <= 296 ? 1.0 : ctas / 296.0;
-    return 5.5 + waves * ceil_div(slabs, parts) * (ctas <= 148 ? 0.5 : 0.75);
-}
+double small_us(int M, int N, bool gated, int slabs) { return plan_small(gated ? kGated : kScaled, M, N, slabs).us; }
+double small_dx_us(int M, int F, int K) { return plan_small(kDx, M, K, 2 * ceil_div(F, 64)).us; }
 
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
@@ -462,8 +523,7 @@ cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaS
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
     const Matrix w1{p.W1 ? p.W1 : p.W, (uint64_t)p.N, K, K};
     const Out out{p.C, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
-    const int slabs = ceil_div(p.K, 128);
-    const Shape shape{p.M, p.N, slabs, slabs, p.act};
+    const Shape shape = shape_of(p.M, p.N, ceil_div(p.K, 128), 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
         if (p.W1) return launch_small<kGated, true, T>(w, w1, a, a, shape, out, err, stream);
         return launch_small<kScaled, true, T>(w, w, a, a, shape, out, err, stream);
@@ -475,8 +535,7 @@ cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStr
     const uint64_t K = p.K, pitch = K * 2;
     const Matrix x{p.X, (uint64_t)p.M, K, pitch}, g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
     const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr};
-    const int slabs = ceil_div(p.K, 64);
-    const Shape shape{p.M, p.F, slabs, slabs, p.act};
+    const Shape shape = shape_of(p.M, p.F, ceil_div(p.K, 64), 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
         return launch_small<kGated, false, T>(g, u, x, x, shape, out, err, stream);
     });
@@ -488,8 +547,7 @@ cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t 
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2};
     const Out out{p.dX, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
-    const int slabs = ceil_div(p.F, 64);
-    const Shape shape{p.M, p.K, slabs, 2 * slabs, 0};
+    const Shape shape = shape_of(p.M, p.K, ceil_div(p.F, 64), 2, 0);
     QG_DISPATCH_16(p.dtype, T, {
         return launch_small<kDx, false, T>(wg, wu, dg, du, shape, out, err, stream);
     });
