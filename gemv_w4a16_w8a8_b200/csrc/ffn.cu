@@ -12,8 +12,11 @@ constexpr int kFewTokens = 64;         // up to here the weights' stream is the 
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
-// elements. Bound: HBM, 10 bytes an element: eight elements a thread by 16-byte loads and stores
-// where F % 8 == 0 (VEC); otherwise one by one.
+// elements, a multiple of eight, which TMA asks for. Bound: HBM, 10 bytes an element. F % 8 == 0: the
+// matrices are one run of eight elements a thread by 16-byte loads and stores. Otherwise rows start
+// anywhere: a CTA takes kSpan elements of a row, by pairs where F is even, else one by one.
+constexpr int kSpan = 2048;
+
 template <typename T, int ACT>
 __device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, uint32_t &dg, uint32_t &du)
 {
@@ -25,42 +28,68 @@ __device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, u
     du = pack2<T>(h2.x * v0, h2.y * v1);
 }
 
-template <typename T, int ACT, bool VEC>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
 grad_act_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__restrict__ U,
-                T *__restrict__ dG, T *__restrict__ dU, int M, int F, int Fp)
+                T *__restrict__ dG, T *__restrict__ dU, size_t n)
 {
     grid_release();
     grid_wait();
-    const size_t at = (size_t)blockIdx.x * kThreads + threadIdx.x;
-    if constexpr (VEC) {
-        if (at >= (size_t)M * F / 8) return;
-        const uint4 h = ld_stream_v4(dH + at * 8), g = ld_stream_v4(G + at * 8), u = ld_stream_v4(U + at * 8);
-        uint4 dg, du;
-        grad_pair<T, ACT>(h.x, g.x, u.x, dg.x, du.x);
-        grad_pair<T, ACT>(h.y, g.y, u.y, dg.y, du.y);
-        grad_pair<T, ACT>(h.z, g.z, u.z, dg.z, du.z);
-        grad_pair<T, ACT>(h.w, g.w, u.w, dg.w, du.w);
-        reinterpret_cast<uint4 *>(dG)[at] = dg;      // F % 8 == 0: Fp == F
-        reinterpret_cast<uint4 *>(dU)[at] = du;
+    const size_t at = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (at >= n) return;
+    const uint4 h = ld_stream_v4(dH + at), g = ld_stream_v4(G + at), u = ld_stream_v4(U + at);
+    uint4 dg, du;
+    grad_pair<T, ACT>(h.x, g.x, u.x, dg.x, du.x);
+    grad_pair<T, ACT>(h.y, g.y, u.y, dg.y, du.y);
+    grad_pair<T, ACT>(h.z, g.z, u.z, dg.z, du.z);
+    grad_pair<T, ACT>(h.w, g.w, u.w, dg.w, du.w);
+    *reinterpret_cast<uint4 *>(dG + at) = dg;
+    *reinterpret_cast<uint4 *>(dU + at) = du;
+}
+
+template <typename T, int ACT, bool PAIRS>
+__global__ void __launch_bounds__(kThreads)
+grad_act_rows_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__restrict__ U,
+                     T *__restrict__ dG, T *__restrict__ dU, int F, int Fp)
+{
+    grid_release();
+    grid_wait();
+    const unsigned spans = (unsigned)(F + kSpan - 1) / kSpan;
+    const size_t m = blockIdx.x / spans;
+    const int f0 = (int)(blockIdx.x % spans) * kSpan, f1 = min(f0 + kSpan, F);
+    const size_t in = m * F, to = m * Fp;
+    if constexpr (PAIRS) {
+#pragma unroll 4
+        for (int f = f0 + 2 * threadIdx.x; f < f1; f += 2 * kThreads) {
+            uint32_t dg, du;
+            grad_pair<T, ACT>(ld_stream_u32(dH + in + f), ld_stream_u32(G + in + f), ld_stream_u32(U + in + f), dg, du);
+            *reinterpret_cast<uint32_t *>(dG + to + f) = dg;
+            *reinterpret_cast<uint32_t *>(dU + to + f) = du;
+        }
     } else {
-        if (at >= (size_t)M * F) return;
-        const size_t m = at / F, to = m * Fp + (at - m * F);
-        float v, d;
-        act_both<ACT>(to_f32(G[at]), v, d);
-        const float dh = to_f32(dH[at]);
-        dG[to] = from_f32<T>(dh * to_f32(U[at]) * d);
-        dU[to] = from_f32<T>(dh * v);
+#pragma unroll 4
+        for (int f = f0 + threadIdx.x; f < f1; f += kThreads) {
+            float v, d;
+            act_both<ACT>(to_f32(G[in + f]), v, d);
+            const float dh = to_f32(dH[in + f]);
+            dG[to + f] = from_f32<T>(dh * to_f32(U[in + f]) * d);
+            dU[to + f] = from_f32<T>(dh * v);
+        }
     }
 }
 
-template <typename T, int ACT, bool VEC> cudaError_t run_grad_act(const GatedGrad &p, cudaStream_t stream)
+template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cudaStream_t stream)
 {
-    const size_t n = (size_t)p.M * p.F / (VEC ? 8 : 1);
-    return launch_dependent(grad_act_kernel<T, ACT, VEC>, dim3((unsigned)((n + kThreads - 1) / kThreads)),
-                            dim3(kThreads), 0, 1, stream, static_cast<const T *>(p.dH),
-                            static_cast<const T *>(p.G), static_cast<const T *>(p.U), static_cast<T *>(p.dG),
-                            static_cast<T *>(p.dU), p.M, p.F, p.Fp);
+    const T *dH = static_cast<const T *>(p.dH), *G = static_cast<const T *>(p.G), *U = static_cast<const T *>(p.U);
+    T *dG = static_cast<T *>(p.dG), *dU = static_cast<T *>(p.dU);
+    const size_t n = (size_t)p.M * p.F, rows = (size_t)p.M * ((p.F + kSpan - 1) / kSpan);
+    const size_t ctas = p.F % 8 ? rows : (n / 8 + kThreads - 1) / kThreads;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)ctas), block(kThreads);
+    if (p.F % 8 == 0) return launch_dependent(grad_act_kernel<T, ACT>, grid, block, 0, 1, stream, dH, G, U, dG, dU, n);
+    if (p.F % 2 == 0)
+        return launch_dependent(grad_act_rows_kernel<T, ACT, true>, grid, block, 0, 1, stream, dH, G, U, dG, dU, p.F, p.Fp);
+    return launch_dependent(grad_act_rows_kernel<T, ACT, false>, grid, block, 0, 1, stream, dH, G, U, dG, dU, p.F, p.Fp);
 }
 
 } // namespace
@@ -87,7 +116,7 @@ cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStr
     cudaError_t e = cudaSuccess;
     QG_DISPATCH_16(p.dtype, T, {
         QG_DISPATCH_ACT(p.act, ACT, {
-            e = p.F % 8 ? run_grad_act<T, ACT, false>(p, stream) : run_grad_act<T, ACT, true>(p, stream);
+            e = run_grad_act<T, ACT>(p, stream);
         });
     });
     if (e == cudaSuccess && p.dX) {
