@@ -151,9 +151,15 @@ def _check(status: int, what: str):
 
 # ---- torch marshalling ------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -465,6 +471,17 @@ def _operand(t, dtype, shape, name, index):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _matrix(t, dtype, name):
+    """_need for a matrix, by the fewest reads where nothing is wrong."""
+    try:
+        if t.dtype is dtype and t.dim() == 2 and t.is_cuda and t.is_contiguous():
+            return t.shape
+    except AttributeError:
+        pass
+    _need(t, dtype, 2, name)
+    return t.shape
+
+
 _HALF_TYPES = None
 
 
@@ -513,11 +530,11 @@ def quant_int8_tokens(X, Q=None, scales=None, stream=None):
     scale = amax / 127, code = rint(x * (127 / amax)) (rule in include/qgemm.h)."""
     torch = _torch()
     dt = _half_type(getattr(X, "dtype", None), "X")
-    _need(X, X.dtype, 2, "X")
+    M, K = _matrix(X, X.dtype, "X")
     if _elsewhere(X, stream):
         with _scope(X, stream):
             return quant_int8_tokens(X, Q, scales)
-    (M, K), dev = X.shape, X.get_device()
+    dev = X.get_device()
     if Q is None:
         Q = torch.empty((M, K), dtype=torch.int8, device=X.device)
     if scales is None:
@@ -534,12 +551,12 @@ def qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias=None, C=None, out_dtype=Non
     C [M,N] = a_scales[m] * w_scales[n] * (A . W^T) (+ bias), in the type of C or of `out_dtype`
     (fp16, the default, or bf16; bias has it too)."""
     torch = _torch()
-    _need(A, torch.int8, 2, "A")
-    _need(W, torch.int8, 2, "W")
+    M, K = _matrix(A, torch.int8, "A")
+    N = _matrix(W, torch.int8, "W")[0]
     if _elsewhere(A, stream):
         with _scope(A, stream):
             return qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias, C, out_dtype)
-    (M, K), N, dev = A.shape, W.shape[0], A.get_device()
+    dev = A.get_device()
     if out_dtype is None:
         out_dtype = torch.float16 if C is None else C.dtype
     dt = _half_type(out_dtype, "out_dtype")
@@ -561,12 +578,12 @@ def qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H=None, act: str =
     H [M,F] = act(gate) * up in the type of H or of `out_dtype` (fp16, the default, or bf16),
     gate and up being the scaled products with Wg and Wu. act: silu, gelu or gelu_tanh."""
     torch = _torch()
-    _need(A, torch.int8, 2, "A")
-    _need(Wg, torch.int8, 2, "Wg")
+    M, K = _matrix(A, torch.int8, "A")
+    F = _matrix(Wg, torch.int8, "Wg")[0]
     if _elsewhere(A, stream):
         with _scope(A, stream):
             return qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H, act, out_dtype)
-    (M, K), F, dev = A.shape, Wg.shape[0], A.get_device()
+    dev = A.get_device()
     if out_dtype is None:
         out_dtype = torch.float16 if H is None else H.dtype
     dt, code = _half_type(out_dtype, "out_dtype"), _activation(act)
@@ -591,14 +608,14 @@ def qgemm_dense_gated(X, Wg, Wu, H=None, G=None, U=None, act: str = "silu",
     torch = _torch()
     dtype = getattr(X, "dtype", None)
     dt, code = _half_type(dtype, "X"), _activation(act)
-    _need(X, dtype, 2, "X")
-    _need(Wg, dtype, 2, "Wg")
+    M, K = _matrix(X, dtype, "X")
+    F = _matrix(Wg, dtype, "Wg")[0]
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
     if _elsewhere(X, stream):
         with _scope(X, stream):
             return qgemm_dense_gated(X, Wg, Wu, H, G, U, act, save_preact)
-    (M, K), F, dev = X.shape, Wg.shape[0], X.get_device()
+    dev = X.get_device()
     save = save_preact or G is not None
     if H is None:
         H = torch.empty((M, F), dtype=dtype, device=X.device)
@@ -627,13 +644,13 @@ def qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U, act: str = "silu", dX=None, 
     torch = _torch()
     dtype = getattr(X, "dtype", None)
     dt, code = _half_type(dtype, "X"), _activation(act)
-    _need(X, dtype, 2, "X")
-    _need(Wg, dtype, 2, "Wg")
+    M, K = _matrix(X, dtype, "X")
+    F = _matrix(Wg, dtype, "Wg")[0]
     if _elsewhere(X, stream):
         with _scope(X, stream):
             return qgemm_dense_gated_backward(dH, X, Wg, Wu, G, U, act, dX, dWg, dWu, need_dx,
                                               need_dw, workspace)
-    (M, K), F, dev = X.shape, Wg.shape[0], X.get_device()
+    dev = X.get_device()
     if need_dx and dX is None:
         dX = torch.empty((M, K), dtype=dtype, device=X.device)
     if need_dw and dWg is None:

@@ -431,17 +431,11 @@ Plan plan_small(int form, int M, int N, int slabs)
         for (int i = 0; i < 4; ++i) {
             const int parts = 1 << i, slots = kClusters[per_sm - 1][i];
             if (parts > 1 && slabs < 4 * parts) break;
-            // even columns over whole waves
-            int waves = 1, cols;
-            for (;; ++waves) {
-                const long long tiles = std::max(1LL, (long long)slots * waves / tiles_t);
-                cols = round_up((int)std::min<long long>((N + tiles - 1) / tiles, N), grain);
-                if (cols <= most) break;
-                if ((long long)slots * waves > (long long)tiles_t * ceil_div(N, most)) {
-                    cols = most;
-                    break;
-                }
-            }
+            // even columns over the fewest whole waves
+            const long long least = (long long)ceil_div(N, most) * tiles_t;
+            const long long waves = (least + slots - 1) / slots;
+            const long long tiles = std::max(1LL, slots * waves / tiles_t);
+            const int cols = round_up((int)((N + tiles - 1) / tiles), grain);
             const long long ctas = (long long)ceil_div(N, cols) * tiles_t * parts;
             const double on_sm = std::max(1.0, std::min(2.0, std::ceil(ctas / 148.0)));
             const double rounds = std::max(1.0, ctas / ((double)kClusters[1][i] * parts));
@@ -450,7 +444,7 @@ Plan plan_small(int form, int M, int N, int slabs)
             const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3, 2.0 / stages_of(used, box)});
             const double sm = ceil_div(slabs, parts) * slab * rounds;
             const double hbm = (double)slabs * kSlab * ((double)N * halves + M) / 6.4e6;
-            const double stream = std::pow(std::pow(sm, 4) + std::pow(hbm, 4), 0.25);
+            const double stream = std::sqrt(std::sqrt(sm * sm * sm * sm + hbm * hbm * hbm * hbm));
             const double tile = on_sm * tokens * used * 4.0;
             const double join = parts > 1 ? 0.5 + 0.15 * parts + tile / 35e3 : tile / 60e3;
             const double us = 2.5 + stream + join * rounds;
