@@ -1,18 +1,19 @@
 // Few tokens: tensor-core kernel of the scaled W8A8 matmul, the gated forward products and dX.
 //
-// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns up to 128 tokens (the MMA's
-// M side; rows past the last token hold whatever follows in shared memory and reach no result) and R
-// rows of the weights (its N side; for kGated R / 2 of the gate and the same of up). R is any multiple
-// of four, so that the weights divide evenly over the SMs: 11008 gate and up columns, say, are 147
-// tiles of 76, where tiles of 64 left 24 of 148 SMs with twice the others' work. An MMA takes about 100
-// cycles for up to 128 rows of 32 bytes and 128 for 256, 40 to 64 B a clock, against the 24 B that HBM
-// delivers to an SM. The ring of 108 KB covers the memory's latency (44 GB/s x 2 us) and leaves room for
-// a second CTA: of this kernel, or of the next on the stream, which sets itself up while this one ends.
+// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns up to 128 tokens and R rows
+// of the weights (for kGated R / 2 of the gate and the same of up). R is any multiple of four, so that
+// the weights divide evenly over the SMs: tiles of 64 gate and up rows left 24 of 148 SMs with twice the
+// others' work at 11008 columns. The ring of 108 KB covers the memory's latency (44 GB/s x 2 us) and
+// leaves room for a second CTA: of this kernel, or of the next on the stream, which sets itself up
+// while this one ends.
 //
-// Device time of calls that follow one another, weights not in L2: one token, 4096 x 11008 int8, 10.4 us
-// (45 MB, 4.3 TB/s); gate and up 11008 x 4096 int8, 17 us (90 MB, 5.3 TB/s); 16 tokens in 16 bits, 30.3 us
-// (181 MB, 6.0 TB/s); 32 tokens, 32000 x 4096, 23.8 us (133 MB, 5.6 TB/s); 16384 x 16384, 41 us (268 MB,
-// 6.5 TB/s). Of each about 3.5 us pass before the first slab arrives and after the last.
+// Orientation (WM): up to 64 tokens the weights are the MMA's M side, in one or two blocks of 128, and
+// the tokens its N side; above, the tokens are the M side and the weights the N side. Unused rows of the
+// M side hold whatever follows in shared memory and reach no result, but the tensor core multiplies them:
+// with 16 tokens in an M of 128 the SMs drew enough power to fall from 1.8 to 1.45 GHz within a tenth of
+// a second, and the stream of weights slowed from 32.4 to 36 us with them. An MMA takes about 100 cycles for
+// up to 128 rows of 32 bytes by up to 128, 128 cycles by 256: 40 to 64 B of weights a clock, against the
+// 24 B that HBM delivers to an SM.
 //
 // Split reduction: the CTAs of a cluster (1, 2, 4 or 8) take consecutive parts of the reduction of
 // one tile, so that a small weight matrix still occupies the device. Each leaves its partial tile
@@ -20,6 +21,11 @@
 // the columns over the cluster (distributed shared memory, parts in order: the same bits every run),
 // applies scales, bias or activation and writes runs of columns of one token. No workspace, no
 // atomics, one launch.
+//
+// Device time of calls that follow one another, weights not in L2: one token, 4096 x 11008 int8, 11.0 us
+// (45 MB, 4.1 TB/s); gate and up 11008 x 4096 int8, 17.1 us (90 MB, 5.3 TB/s); 16 tokens in 16 bits, 30.6 us
+// (181 MB, 5.9 TB/s); 32 tokens, 32000 x 4096, 24.7 us (133 MB, 5.4 TB/s); 16384 x 16384, 41.8 us (268 MB,
+// 6.4 TB/s). Of each about 3.5 us pass before the first slab arrives and after the last.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -34,7 +40,8 @@ enum Form { kScaled, kGated, kDx };
 
 constexpr int kThreads = 192;          // warps 0-3 accumulator and output, 4 TMA, 5 MMA
 constexpr int kOutThreads = 128;
-constexpr int kTokens = 128, kSlab = 128;
+constexpr int kTokens = 128, kSlab = 128, kMmaM = 128;
+constexpr int kWeightMajor = 64;       // up to so many tokens the weights are the MMA's M side
 constexpr int kRingBytes = 108 * 1024;
 constexpr int kMaxStages = 16;
 
@@ -47,7 +54,7 @@ struct Shape {
     int M, N;               // tokens; columns of the result
     int cols;               // result columns of a tile, a multiple of 4
     int second;             // first row of up in a slab, a multiple of 8 (kGated)
-    int rows;               // the MMA's N, a multiple of 16
+    int used;               // weight rows in a slab that reach a result
     int slab_rows;          // weight rows in a slab, a multiple of 8
     int box_tokens;         // token rows in a slab, a multiple of 8
     int stages;
@@ -78,11 +85,11 @@ __device__ __forceinline__ void mma_one(uint32_t dtm, uint64_t a, uint64_t b, ui
                      : "memory");
 }
 
-template <bool I8, typename T, bool BMN> __device__ __forceinline__ uint32_t instr_desc(int n)
+template <bool I8, typename T, bool AMN, bool BMN> __device__ __forceinline__ uint32_t instr_desc(int n)
 {
     constexpr uint32_t in = I8 ? 1u : (std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
-    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (BMN ? 1u : 0u) << 16 | (uint32_t)(n >> 3) << 17 |
-           (uint32_t)(kTokens >> 4) << 24;
+    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (AMN ? 1u : 0u) << 15 | (BMN ? 1u : 0u) << 16 |
+           (uint32_t)(n >> 3) << 17 | (uint32_t)(kMmaM >> 4) << 24;
 }
 
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr)
@@ -108,25 +115,31 @@ __device__ __forceinline__ void store4(T *row, int n, int N, const float (&r)[4]
     }
 }
 
-template <int FORM, bool I8, typename T>
+template <int FORM, bool I8, typename T, bool WM>
 __global__ void __launch_bounds__(kThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ CUtensorMap tm_w1,
              const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
              const Shape shape, const Out out, unsigned int *err)
 {
     using Acc = typename std::conditional<I8, int, float>::type;
-    constexpr bool BMN = FORM == kDx;
+    constexpr bool WMN = FORM == kDx;              // MN-major weights
     constexpr int kElems = I8 ? 128 : 64;
     const int ST = shape.stages, N = shape.N;
-    // (the MMA's last rows may reach past a slab: into the next one or the 8 rows behind the ring)
     const int x_bytes = shape.box_tokens * kSlab, w_bytes = shape.slab_rows * kSlab;
-    const uint32_t cols_alloc = shape.rows <= 32 ? 32u : (shape.rows <= 64 ? 64u : (shape.rows <= 128 ? 128u : 256u));
+    // the MMA's N, and accumulator columns: of each block of 128 weight rows (WM), or of the weights
+    const int mma_n = ((WM ? shape.box_tokens : shape.used) + 15) / 16 * 16;
+    const int blocks = WM ? (shape.used + kMmaM - 1) / kMmaM : 1;
+    const int acc_cols = mma_n * blocks;
+    const uint32_t cols_alloc = acc_cols <= 32 ? 32u : (acc_cols <= 64 ? 64u : (acc_cols <= 128 ? 128u : 256u));
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    // token slabs first: the MMA reads 128 rows from the start of one, always inside the ring
-    const uint32_t ring_x = smem_u32(base), ring_w = ring_x + ST * x_bytes;
+    // The slabs of the M side first: the MMA reads whole blocks of 128 rows from the start of one, which
+    // reach into later slabs and into the N side's; the N side's last slab, 8 rows at most, into the
+    // rows behind the ring.
+    const uint32_t ring_m = smem_u32(base), ring_n = ring_m + ST * (WM ? w_bytes : x_bytes);
+    const uint32_t ring_w = WM ? ring_m : ring_n, ring_x = WM ? ring_n : ring_m;
     float *scale_s = reinterpret_cast<float *>(base + kScaleOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + kBarOff);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
@@ -168,7 +181,7 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         const bool second = FORM == kDx && s0 + i >= shape.seg_slabs;
         const int k = (s0 + i - (second ? shape.seg_slabs : 0)) * kElems;
         if constexpr (FORM == kDx) {
-            for (int c = 0; c < shape.rows; c += 64) copy(c * kSlab, second ? &tm_w1 : &tm_w0, n0 + c, k);
+            for (int c = 0; c < shape.used; c += 64) copy(c * kSlab, second ? &tm_w1 : &tm_w0, n0 + c, k);
         } else {
             copy(0, &tm_w0, k, n0);
             if constexpr (FORM == kGated) copy(shape.second * kSlab, &tm_w1, k, n0);
@@ -217,7 +230,7 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 
     if (warp == 4) {
         // ---------------- TMA producer ----------------
-        const uint32_t tx = (uint32_t)x_bytes + (FORM == kGated ? 2 * shape.cols : (FORM == kDx ? shape.rows : shape.cols)) * kSlab;
+        const uint32_t tx = (uint32_t)x_bytes + (FORM == kGated ? 2 : 1) * shape.cols * kSlab;
         int it = 0, s = 0;
         uint32_t phase = 1;
         for (; it < ns; ++it) {
@@ -248,20 +261,28 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         }
     } else if (warp == 5) {
         // ---------------- MMA issue ----------------
-        const uint32_t idesc = instr_desc<I8, T, BMN>(shape.rows);
+        const uint32_t idesc = instr_desc<I8, T, WM && WMN, !WM && WMN>(mma_n);
+        constexpr int kw = WMN ? 128 : 2;          // 16 rows of an MN-major slab, or 32 bytes of a K-major one
         int s = 0;
         uint32_t phase = 0;
         for (int it = 0; it < ns; ++it) {
             const uint64_t dx = sw128_desc(ring_x + s * x_bytes);
             const uint32_t wa = ring_w + s * w_bytes;
-            const uint64_t dw = BMN ? sw128_desc_mn(wa, 8192) : sw128_desc(wa);
+            const uint64_t dw = WMN ? sw128_desc_mn(wa, 8192) : sw128_desc(wa);
             if (!warp_wait(full_bar(s), phase, abort_flag, err)) break;
             tc_fence_after();
-            constexpr int kw = BMN ? 128 : 2;
             if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_one<I8>(tmem_base, dx + 2 * k, dw + kw * k, idesc, (it | k) != 0 ? 1u : 0u);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t accumulate = (it | k) != 0 ? 1u : 0u;
+                    if constexpr (WM) {
+                        mma_one<I8>(tmem_base, dw + kw * k, dx + 2 * k, idesc, accumulate);
+                        // the next 128 rows: 16 KB on, in either layout
+                        if (blocks > 1) mma_one<I8>(tmem_base + mma_n, dw + kw * k + 1024, dx + 2 * k, idesc, accumulate);
+                    } else {
+                        mma_one<I8>(tmem_base, dx + 2 * k, dw + kw * k, idesc, accumulate);
+                    }
+                }
                 mma_commit(empty_bar(s));
             }
             __syncwarp();
@@ -275,24 +296,39 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         int dummy_abort = 0;
         mbar_wait(done_bar, 0, &dummy_abort, nullptr);
     }
-    // The accumulator to shared memory as [token][weight row]: lane = token. A CTA whose waits
-    // gave up has raised the error word; it goes through the same steps so that nobody hangs.
+    // The accumulator to shared memory as [token][weight row]: lane = weight row (WM) or token. A CTA whose
+    // waits gave up has raised the error word; it goes through the same steps so that nobody hangs.
     if (warp < 4) mbar_wait(done_bar, 0, abort_flag, err);
     __syncthreads();               // the copies have landed and the MMAs have read them
-    if (warp * 32 < tokens && warp < 4) {
+    uint32_t *part = reinterpret_cast<uint32_t *>(base);
+    if (warp < 4) {
         tc_fence_after();
         const uint32_t tm = tmem_base + ((uint32_t)(warp * 32) << 16);
-        uint32_t *row = reinterpret_cast<uint32_t *>(base) + (size_t)threadIdx.x * shape.pitch;
-        const int used = FORM == kGated ? shape.second + shape.cols : shape.cols;
+        if constexpr (WM) {
+            for (int b = 0; b < blocks; ++b) {
+                const int row = b * kMmaM + (int)threadIdx.x;
 #pragma unroll 1
-        for (int c = 0; c < used; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(tm + c, v);
-            if ((int)threadIdx.x < tokens)
+                for (int c = 0; c < tokens; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tm + b * mma_n + c, v);
+                    if (row < shape.used)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c + 4 * q < used)
-                        *reinterpret_cast<uint4 *>(row + c + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        for (int q = 0; q < 16; ++q)
+                            if (c + q < tokens) part[(c + q) * shape.pitch + row] = v[q];
+                }
+            }
+        } else if (warp * 32 < tokens) {
+            uint32_t *to = part + threadIdx.x * shape.pitch;
+#pragma unroll 1
+            for (int c = 0; c < shape.used; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tm + c, v);
+                if ((int)threadIdx.x < tokens)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + 4 * q < shape.used)
+                            *reinterpret_cast<uint4 *>(to + c + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
         }
         tc_fence_before();
     }
@@ -301,9 +337,9 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     else __syncthreads();
 
     if (warp < 4 && mine) {
-        const uint32_t part = smem_u32(base) + (uint32_t)(n - n0) * 4;
+        const uint32_t group = smem_u32(part) + (uint32_t)(n - n0) * 4;
         auto total = [&](int token, int shift, Acc (&r)[4]) {
-            const uint32_t at = part + (uint32_t)(token * shape.pitch + shift) * 4;
+            const uint32_t at = group + (uint32_t)(token * shape.pitch + shift) * 4;
             uint4 v[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p)          // all in flight before the first is added
@@ -392,9 +428,16 @@ template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, int 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int round_up(int a, int b) { return ceil_div(a, b) * b; }
 
-int stages_of(int used, int box)
+// Stages of the ring: its bytes, and the whole blocks of 128 rows that the MMA reads from the last
+// slab of the M side.
+int stages_of(int used, int box, int M)
 {
-    return std::min(kMaxStages, kRingBytes / ((round_up(used, 8) + box) * kSlab));
+    const int w = round_up(used, 8) * kSlab, x = box * kSlab;
+    int st = std::min(kMaxStages, kRingBytes / (w + x));
+    const bool wm = M <= kWeightMajor;
+    const int first = wm ? w : x, read = wm ? round_up(used, kMmaM) * kSlab : kMmaM * kSlab;
+    while (st > 2 && (st - 1) * first + read > kRingBytes) --st;
+    return st;
 }
 
 struct Plan {
@@ -409,14 +452,14 @@ constexpr int kClusters[2][4] = {{148, 74, 33, 15}, {296, 148, 71, 33}};
 // Columns of a tile and parts of the reduction: for every cluster size and one or two CTAs an SM, the
 // columns that divide the weights evenly over the clusters that run at once (more waves of them if a
 // tile's columns would not fit), by the estimated time of
-//   - a slab: its four MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together;
-//     more beyond 128 and 170 rows), what L2 delivers to an SM (115 GB/s), or the memory's 2 us over the
-//     slabs in flight;
+//   - a slab: its MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together; more
+//     with a second block or a wide N side), what L2 delivers to an SM (115 GB/s), or the memory's 2 us
+//     over the slabs in flight;
 //   - the stream: the slabs of a CTA against HBM, the two slowing each other near balance;
 //   - joining: a barrier, and partial tiles through shared memory at 35 GB/s (60 GB/s unsplit).
 // Times in us of columns x parts, measured over a sweep: one token, 11008 gate and up columns, 4096 deep,
-// 76x1: 17.3, 40x1: 17.8, 64x1: 18.7, 128x1: 20.1; 16 tokens in 16 bits, 76x2: 31.1, 64x1: 33.1,
-// 76x1: 34.4; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5, 64x2: 10.6.
+// 76x2: 17.1, 76x1: 17.8, 40x1: 17.8, 64x1: 19.1, 128x1: 19.4; 16 tokens in 16 bits, 76x2: 30.6, 40x1:
+// 32.7, 64x1: 33.4, 76x1: 34.7; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5, 64x2: 10.6.
 Plan plan_small(int form, int M, int N, int slabs)
 {
     const int tiles_t = ceil_div(M, kTokens), box = round_up(std::min(M, kTokens), 8);
@@ -440,8 +483,10 @@ Plan plan_small(int form, int M, int N, int slabs)
             const double on_sm = std::max(1.0, std::min(2.0, std::ceil(ctas / 148.0)));
             const double rounds = std::max(1.0, ctas / ((double)kClusters[1][i] * parts));
             const int used = form == kGated ? round_up(cols, 8) + cols : cols, tokens = std::min(M, kTokens);
-            const double mma = on_sm < 2 ? 0.29 + (used > 128 ? 0.06 : 0) : 0.40 * std::max(1.0, used / 170.0);
-            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3, 2.0 / stages_of(used, box)});
+            const int blocks = M <= kWeightMajor ? ceil_div(used, kMmaM) : 1;
+            const double mma = on_sm < 2 ? (blocks > 1 ? 0.40 : (used > 128 ? 0.35 : 0.29))
+                                         : (blocks > 1 ? 0.50 : 0.40 * std::max(1.0, used / 170.0));
+            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3, 2.0 / stages_of(used, box, M)});
             const double sm = ceil_div(slabs, parts) * slab * rounds;
             const double hbm = (double)slabs * kSlab * ((double)N * halves + M) / 6.4e6;
             const double stream = std::sqrt(std::sqrt(sm * sm * sm * sm + hbm * hbm * hbm * hbm));
@@ -453,11 +498,11 @@ Plan plan_small(int form, int M, int N, int slabs)
     return best;
 }
 
-template <int FORM, bool I8, typename T>
-cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
-                         Shape shape, const Out &out, unsigned int *err, cudaStream_t stream)
+template <int FORM, bool I8, typename T, bool WM>
+cudaError_t launch_plan(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
+                        Shape shape, const Out &out, unsigned int *err, cudaStream_t stream)
 {
-    auto kern = small_kernel<FORM, I8, T>;
+    auto kern = small_kernel<FORM, I8, T, WM>;
     static std::mutex mu;
     static bool opted_in[64] = {};
     int dev = 0;
@@ -473,13 +518,12 @@ cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, c
     const Plan plan = plan_small(FORM, shape.M, shape.N, shape.slabs);
     shape.cols = plan.cols;
     shape.second = FORM == kGated ? round_up(plan.cols, 8) : 0;
-    const int used = shape.second + plan.cols;
-    shape.rows = round_up(used, 16);
+    const int used = shape.used = shape.second + plan.cols;
     shape.box_tokens = round_up(std::min(shape.M, kTokens), 8);
     shape.pitch = used / 4 % 2 ? used : used + 4;
     shape.slab_rows = round_up(used, 8);
-    shape.stages = stages_of(used, shape.box_tokens);
-    if (std::min(shape.M, kTokens) * shape.pitch * 4 > kRingBytes || shape.rows > 256 || shape.stages < 2)
+    shape.stages = stages_of(used, shape.box_tokens, shape.M);
+    if (std::min(shape.M, kTokens) * shape.pitch * 4 > kRingBytes || used > 256 || shape.stages < 2)
         return cudaErrorInvalidConfiguration;
     const long long tiles = (long long)ceil_div(shape.N, plan.cols) * ceil_div(shape.M, kTokens);
     if (tiles * plan.parts > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -493,6 +537,14 @@ cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, c
     if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, shape.box_tokens)) return cudaErrorInvalidValue;
     return launch_dependent(kern, dim3((unsigned)(tiles * plan.parts)), dim3(kThreads), kSmem, plan.parts, stream,
                             tw0, tw1, tx0, tx1, shape, out, err);
+}
+
+template <int FORM, bool I8, typename T>
+cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
+                         const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
+{
+    if (shape.M <= kWeightMajor) return launch_plan<FORM, I8, T, true>(w0, w1, x0, x1, shape, out, err, stream);
+    return launch_plan<FORM, I8, T, false>(w0, w1, x0, x1, shape, out, err, stream);
 }
 
 Shape shape_of(int M, int N, int seg_slabs, int segs, int act)
