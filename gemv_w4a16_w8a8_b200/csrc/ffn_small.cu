@@ -332,9 +332,16 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         }
         tc_fence_before();
     }
-    __syncwarp();
+    __syncthreads();
+    // TMEM goes back before this CTA waits for others of its cluster: a kernel of another stream whose
+    // CTAs wait for it on one SM while theirs keep a CTA of this cluster waiting on another would
+    // otherwise never see it freed.
+    if (warp == 5) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(cols_alloc)
+                     : "memory");
+    }
     if (cl > 1) cluster_sync();
-    else __syncthreads();
 
     if (warp < 4 && mine) {
         const uint32_t group = smem_u32(part) + (uint32_t)(n - n0) * 4;
@@ -402,12 +409,6 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     __syncwarp();
     // no CTA may leave while another reads its shared memory
     if (cl > 1) cluster_sync();
-    else __syncthreads();
-    if (warp == 5) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(cols_alloc)
-                     : "memory");
-    }
 }
 
 // ---- host side -------------------------------------------------------------------------------------

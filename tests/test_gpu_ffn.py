@@ -85,7 +85,8 @@ def test_quant_special_rows(dtype):
 SCALED_SHAPES = [(1, 1, 16), (1, 256, 4096), (2, 129, 48), (4, 4096, 512), (5, 1000, 1040), (8, 333, 2064),
                  (16, 512, 11008), (17, 130, 64), (31, 777, 4112), (33, 4100, 256), (64, 128, 8192), (77, 1371, 528),
                  (128, 257, 128), (129, 1024, 4096), (255, 640, 272), (300, 2001, 1024), (513, 776, 2064),
-                 (1000, 3000, 400), (2049, 1288, 512)]
+                 (1000, 3000, 400), (2049, 1288, 512), (64, 4096, 1024), (65, 4097, 1024), (96, 100, 2048),
+                 (3, 100001, 64), (20, 32000, 144), (200, 70, 16384), (700, 200, 4096), (5000, 33, 48)]
 
 
 def scaled_case(M, N, K, dtype, bias, seed=0):
@@ -236,7 +237,8 @@ def test_gated_non_finite_stay_in_their_row_and_column():
 
 BWD_SHAPES = [(1, 1, 8), (1, 256, 512), (2, 65, 24), (3, 100, 40), (16, 512, 1024), (33, 777, 136), (64, 64, 64),
               (77, 1371, 520), (128, 256, 256), (129, 1000, 264), (255, 130, 2056), (300, 2001, 104), (513, 776, 520),
-              (1000, 65, 8), (2049, 520, 136), (40, 4103, 72)]
+              (1000, 65, 8), (2049, 520, 136), (40, 4103, 72), (4000, 100, 64), (700, 4098, 256), (64, 1030, 2048),
+              (8, 9000, 512), (1500, 260, 1032)]
 
 
 def backward_case(M, F, K, dtype, seed=0):
@@ -412,6 +414,12 @@ def test_other_streams_and_two_at_once():
     torch.cuda.synchronize()
     for o, w in zip((o1, o2), want):
         assert all(torch.equal(v, w[k]) for k, v in o.items())
+    torch.cuda.synchronize()
+    clear(o1)
+    torch.cuda.synchronize()
+    c1(0)                                      # the legacy default stream, by its handle
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[0][k]) for k, v in o1.items())
     # buffers that the call makes itself belong to the stream that it runs on
     x = torch.ones(4, 64, dtype=torch.float16, device=DEV)
     q, s = qg.quant_int8_tokens(x, stream=s1)
