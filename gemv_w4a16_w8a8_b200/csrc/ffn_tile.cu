@@ -151,15 +151,27 @@ __device__ __forceinline__ void stage_flush(const uint8_t *stage, E *c, size_t l
                 *reinterpret_cast<uint4 *>(c + (size_t)r * ld + j * kPer) = v;
         }
     } else {
-        // 4-byte elements fill half a warp's lanes: two rows an instruction
-        constexpr int kAt = 32 / kCols;
-        const int q = lane % kCols;
-#pragma unroll 8
-        for (int r0 = 0; r0 < 32; r0 += kAt) {
-            const int r = r0 + lane / kCols;
-            if (r < rows && q < cols)
-                c[(size_t)r * ld + q] = *reinterpret_cast<const E *>(
-                    stage + r * 64 + (((q / kPer) ^ (r >> 1 & 3)) << 4) + (q % kPer) * sizeof(E));
+        // 4-byte elements fill half a warp's lanes: two rows an instruction. Eight loads, then their
+        // stores, from a pointer that moves down the rows.
+        constexpr int kAt = 32 / kCols, kBatch = 8;
+        const int q = lane % kCols, r0 = lane / kCols;
+        const uint8_t *from = stage + r0 * 64 + (q % kPer) * sizeof(E);
+        E *to = c + (size_t)r0 * ld + q;
+        const size_t down = (size_t)kAt * ld;
+        const int full = q < cols ? rows : 0;
+#pragma unroll 1
+        for (int r = r0; r < 32; r += kAt * kBatch) {
+            E v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = r + i * kAt;
+                v[i] = *reinterpret_cast<const E *>(from + (at - r0) * 64 + (((q / kPer) ^ (at >> 1 & 3)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (r + i * kAt < full) *to = v[i];
+                to += down;
+            }
         }
     }
     __syncwarp();
@@ -346,32 +358,42 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         const int quarter = warp & 3, first = 32 * (warp >> 2);
         const int N = shape.N;
         const bool vec = (N & 7) == 0;
+        // A lane's row scale, and the factors of column c + lane of a tile: the two scales of kGated, or
+        // scale and bias. A tile's first ones are loaded while the tile before it is written.
+        float sa = 0.f, f0 = 0.f, f1 = 0.f;
+        auto factors = [&](const Unit &w, int c) {
+            const int n = min(w.n0 + min(c + lane, ncol - 1), N - 1);
+            f0 = out.sw[n];
+            if constexpr (FORM == kGated) f1 = out.sw1[n];
+            else f1 = out.bias ? to_f32(static_cast<const T *>(out.bias)[n]) : 0.f;
+        };
+        auto first_row = [&](const Unit &w) { return w.m0 + (int)rank * kRows + quarter * 32; };
+        auto row_scale = [&](const Unit &w) {
+            const int m = first_row(w) + lane;
+            return m < shape.M ? out.sa[m] : 0.f;
+        };
+        Unit next = unit_of(ustart, shape, ncol);
+        float sa_next = 0.f;
+        if constexpr (I8) {
+            sa_next = row_scale(next);
+            factors(next, first);
+        }
         int j = 0;
         for (int u = ustart; u < shape.units; u += ustep, ++j) {
-            const Unit w = unit_of(u, shape, ncol);
+            const Unit w = next;
             const int b = j & 1;
-            const int m = w.m0 + (int)rank * kRows + quarter * 32;    // the warp's first row
+            const int m = first_row(w);                               // the warp's first row
             const int rows = min(32, shape.M - m);
             const int nc = min(ncol, N - w.n0);
-            // a lane's row scale, and the factors of column c + lane: the two scales of kGated, or
-            // scale and bias
-            float sa = 0.f, f0 = 0.f, f1 = 0.f;
-            auto factors = [&](int c) {
-                const int n = w.n0 + min(c + lane, nc - 1);
-                f0 = out.sw[n];
-                if constexpr (FORM == kGated) f1 = out.sw1[n];
-                else f1 = out.bias ? to_f32(static_cast<const T *>(out.bias)[n]) : 0.f;
-            };
-            if constexpr (I8) {
-                if (lane < rows) sa = out.sa[m + lane];
-                factors(first);
-            }
+            sa = sa_next;
+            if (u + ustep < shape.units) next = unit_of(u + ustep, shape, ncol);
+            if constexpr (I8) sa_next = row_scale(next);
             bool ok = mbar_wait(accf_bar(b), (j >> 1) & 1, abort_flag, err);
             tc_fence_after();
             ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             if (!ok) break;
             const uint32_t tm = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * kMaxBn);
-            if (rows > 0) {
+            if (rows > 0 && first < nc) {
 #pragma unroll 1
                 for (int c = first; c < nc; c += 64) {
                     uint32_t v[32], z[32];
@@ -381,7 +403,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                         col[lane] = f0;
                         col[32 + lane] = f1;
                         __syncwarp();
-                        if (c + 64 < nc) factors(c + 64);
+                        if (c + 64 < nc) factors(w, c + 64);
+                        else factors(next, first);
                     }
                     tmem_wait_ld();
                     const int cols = nc - c;
@@ -392,10 +415,34 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                         else     // pairs of elements
                             stage_flush(stage, reinterpret_cast<uint32_t *>(dst), N / 2, rows, cols / 2, lane, false);
                     };
-                    // an int32 sum scaled by its row and then its column, as the definition has it
-                    auto scaled = [&](uint32_t x, float f) {
-                        return __fmul_rn(__fmul_rn(__int2float_rn((int)x), sa), f);
-                    };
+                    // int32 sums to fp32, scaled by their row and then their column, as the definition
+                    // has it; then the bias
+                    if constexpr (I8) {
+                        auto scale = [&](uint32_t (&x)[32], int at) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 f = reinterpret_cast<const float4 *>(col)[at / 4 + q];
+                                const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    x[4 * q + e] = __float_as_uint(
+                                        __fmul_rn(__fmul_rn(__int2float_rn((int)x[4 * q + e]), sa), fs[e]));
+                            }
+                        };
+                        scale(v, 0);
+                        if constexpr (FORM == kGated) {
+                            scale(z, 32);
+                        } else if (out.bias) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 f = reinterpret_cast<const float4 *>(col)[8 + q];
+                                const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    v[4 * q + e] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * q + e]), fs[e]));
+                            }
+                        }
+                    }
                     uint32_t hw[16];
                     if constexpr (FORM == kGated) {
                         uint32_t gw[16], uw[16];
@@ -403,17 +450,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                             constexpr int ACT = decltype(act)::value;
 #pragma unroll
                             for (int q = 0; q < 16; ++q) {
-                                float g[2], x[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    if constexpr (I8) {
-                                        g[e] = scaled(v[2 * q + e], col[2 * q + e]);
-                                        x[e] = scaled(z[2 * q + e], col[32 + 2 * q + e]);
-                                    } else {
-                                        g[e] = __uint_as_float(v[2 * q + e]);
-                                        x[e] = __uint_as_float(z[2 * q + e]);
-                                    }
-                                }
+                                const float g[2] = {__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])};
+                                const float x[2] = {__uint_as_float(z[2 * q]), __uint_as_float(z[2 * q + 1])};
                                 hw[q] = pack2<T>(act_value<ACT>(g[0]) * x[0], act_value<ACT>(g[1]) * x[1]);
                                 gw[q] = pack2<T>(g[0], g[1]);
                                 uw[q] = pack2<T>(x[0], x[1]);
@@ -429,19 +467,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                                 write(uw, out.c2);
                             }
                         }
-                    } else if constexpr (I8) {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            float r[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                r[e] = scaled(v[2 * q + e], col[2 * q + e]);
-                                if (out.bias) r[e] = __fadd_rn(r[e], col[32 + 2 * q + e]);
-                            }
-                            hw[q] = pack2<T>(r[0], r[1]);
-                        }
-                        write(hw, out.c0);
-                    } else if (shape.parts > 1) {
+                    } else if (FORM != kScaled && shape.parts > 1) {
                         float *dst = out.part + ((size_t)(w.which * shape.parts + w.part) * shape.M + m) * N + w.n0 + c;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -459,10 +485,12 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                     if constexpr (I8) __syncwarp();       // the column factors are read
                 }
             }
-            // the accumulator goes back to the MMA warp (of the pair's first CTA)
+            else if constexpr (I8) factors(next, first);
+            // The accumulator goes back to the MMA warp (of the pair's first CTA). All that this orders
+            // are reads of TMEM that have returned; a release would wait for the results' stores.
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(b), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(acce_bar(b), 0));
         }
     }
 
