@@ -287,6 +287,13 @@ qg_status qgemm_dense_f16(const void *A, const void *W, void *C, int M, int N, i
 /* ---- 8-bit activations with scales; the gated feed-forward block ------------------------------ */
 
 /*
+ * The entry points of this section choose their kernels by themselves (no pinned configurations) and
+ * take any M, N and F. Their results are the same bit for bit from run to run. Consecutive calls on
+ * a stream overlap one call's set-up with the end of the one before; stream order is kept. Kernels are
+ * loaded at their first use on a device: make a first call of the same kind before a stream capture.
+ */
+
+/*
  * Quantise 16-bit activations to int8 with one scale a token. X: fp16 / bf16 [M, K] (dtype).
  * Q: int8 [M, K]; scales: fp32 [M]. Per row, every step a binary32 operation rounded to nearest:
  *     amax = max_k |x|,  s = amax / 127 (1 for a row of zeros),  q = rint(x * (127 / amax)),
@@ -304,7 +311,7 @@ qg_status quant_int8_tokens(const void *X, int8_t *Q, float *scales, int M, int 
  *     C[m, n] = a_scales[m] * w_scales[n] * sum_k A[m, k] W[n, k] (+ bias[n])
  * The sum is exact in int32; its conversion, the two products (a_scales first) and the bias's
  * addition are binary32 operations; one rounding to `dtype` at the end. Any int8 value is
- * allowed. The result is the same bit for bit from run to run.
+ * allowed.
  * Requires K % 16 == 0, K < 131072 (above it the sum could leave int32); A, W, C 16-byte
  * aligned, scales 4-byte, bias 2-byte aligned.
  */
@@ -317,7 +324,7 @@ qg_status qgemm_w8a8_scaled(const int8_t *A, const int8_t *W, const float *a_sca
  * Wg, Wu: int8 [F, K]; a_scales: fp32 [M]; g_scales, u_scales: fp32 [F]; H: `dtype` [M, F].
  *     g = a_scales[m] g_scales[f] sum_k A Wg,   u = a_scales[m] u_scales[f] sum_k A Wu,
  *     H[m, f] = act(g) * u                      (act: qg_act; fp32, rounded once)
- * Requirements and reproducibility as qgemm_w8a8_scaled, with F for N.
+ * Requirements as qgemm_w8a8_scaled, with F for N.
  */
 qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
                            const float *a_scales, const float *g_scales, const float *u_scales,
@@ -328,8 +335,7 @@ qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
  *     G = X Wg^T,  U = X Wu^T,  H = act(G) * U     [M, F]
  * G and U: NULL, or both given for training: they receive the pre-activations, rounded to
  * `dtype`, that qgemm_dense_gated_backward reads (H is formed from the unrounded ones).
- * Requires K % 8 == 0; every pointer 16-byte aligned. The result is the same bit for bit from
- * run to run.
+ * Requires K % 8 == 0; every pointer 16-byte aligned.
  */
 qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void *H, void *G,
                             void *U, int M, int F, int K, int act, int dtype,
@@ -344,8 +350,7 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
  * workspace: caller-owned device memory, 256-byte aligned, at least
  * qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes, contents on entry and after the
  * call of no meaning. Calls that share a workspace must not overlap on the GPU. Outputs must
- * not overlap inputs. Requires K % 8 == 0; every pointer 16-byte aligned. The result is the
- * same bit for bit from run to run.
+ * not overlap inputs. Requires K % 8 == 0; every pointer 16-byte aligned.
  */
 qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
                                      const void *G, const void *U, void *dX, void *dWg, void *dWu,
