@@ -6,8 +6,8 @@
 // so that a CTA takes eight; a CTA of 128 or 512 for longer ones), which hold it in registers
 // between the maximum and the rounding: it is read once up to 16384 values, and a second time,
 // from L2, beyond.
-//   - The maximum is taken on the bit patterns without their sign, two values a SIMD instruction: as
-//     integers they are ordered like the magnitudes, infinities and NaNs above every number.
+//   - The maximum is taken on the bit patterns without their sign, two values a SIMD instruction:
+//     as integers they are ordered like the magnitudes, infinities and NaNs above every number.
 //   - Rounding adds 1.5 * 2^23 in fp32: the sum's unit is 1, so the addition rounds to the nearest
 //     integer, ties to even, and its low byte is the code in two's complement. Conversion
 //     instructions run at an eighth of this rate and would take half of the kernel's time.
@@ -36,7 +36,9 @@ template <typename T>
 __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float up, float inv)
 {
     const float2 a = unpack2<T>(lo), b = unpack2<T>(hi);
-    auto code = [&](float x) { return __float_as_uint(__fadd_rn(__fmul_rn(x * up, inv), 12582912.0f)); };
+    auto code = [&](float x) {
+        return __float_as_uint(__fadd_rn(__fmul_rn(x * up, inv), 12582912.0f));
+    };
     return prmt(prmt(code(a.x), code(a.y), 0x0040), prmt(code(b.x), code(b.y), 0x0040), 0x5410);
 }
 
@@ -66,7 +68,8 @@ quant_tokens_kernel(const T *__restrict__ X, int8_t *__restrict__ Q, float *__re
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (t + i * TPR < n) v[i] = LONG ? ld_cached_v4(x + t + i * TPR) : ld_stream_v4(x + t + i * TPR);
+        if (t + i * TPR < n)
+            v[i] = LONG ? ld_cached_v4(x + t + i * TPR) : ld_stream_v4(x + t + i * TPR);
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) top = max_abs(top, v[i]);
@@ -99,8 +102,9 @@ template <typename T, int TPR, bool LONG>
 cudaError_t run(const void *X, int8_t *Q, float *scales, int M, int K, cudaStream_t stream)
 {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR;
-    return launch_dependent(quant_tokens_kernel<T, TPR, LONG>, dim3((unsigned)((M + (long long)kRows - 1) / kRows)),
-                            dim3(kThreads), 0, 1, stream, static_cast<const T *>(X), Q, scales, M, K);
+    const dim3 grid((unsigned)((M + (long long)kRows - 1) / kRows));
+    return launch_dependent(quant_tokens_kernel<T, TPR, LONG>, grid, dim3(kThreads), 0, 1, stream,
+                            static_cast<const T *>(X), Q, scales, M, K);
 }
 
 } // namespace

@@ -12,13 +12,14 @@ constexpr int kFewTokens = 64;         // up to here the weights' stream is the 
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
-// elements, a multiple of eight, which TMA asks for. Bound: HBM, 10 bytes an element. F % 8 == 0: the
-// matrices are one run of eight elements a thread by 16-byte loads and stores. Otherwise rows start
-// anywhere: a CTA takes kSpan elements of a row, by pairs where F is even, else one by one.
+// elements, a multiple of eight, which TMA asks for. Bound: HBM, 10 bytes an element. F % 8 == 0:
+// the matrices are one run of eight elements a thread by 16-byte loads and stores. Otherwise rows
+// start anywhere: a CTA takes kSpan elements of a row, by pairs where F is even, else one by one.
 constexpr int kSpan = 2048;
 
 template <typename T, int ACT>
-__device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, uint32_t &dg, uint32_t &du)
+__device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, uint32_t &dg,
+                                          uint32_t &du)
 {
     const float2 h2 = unpack2<T>(dh), g2 = unpack2<T>(g), u2 = unpack2<T>(u);
     float v0, d0, v1, d1;
@@ -62,7 +63,8 @@ grad_act_rows_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T 
 #pragma unroll 4
         for (int f = f0 + 2 * threadIdx.x; f < f1; f += 2 * kThreads) {
             uint32_t dg, du;
-            grad_pair<T, ACT>(ld_stream_u32(dH + in + f), ld_stream_u32(G + in + f), ld_stream_u32(U + in + f), dg, du);
+            grad_pair<T, ACT>(ld_stream_u32(dH + in + f), ld_stream_u32(G + in + f),
+                              ld_stream_u32(U + in + f), dg, du);
             *reinterpret_cast<uint32_t *>(dG + to + f) = dg;
             *reinterpret_cast<uint32_t *>(dU + to + f) = du;
         }
@@ -80,16 +82,20 @@ grad_act_rows_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T 
 
 template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cudaStream_t stream)
 {
-    const T *dH = static_cast<const T *>(p.dH), *G = static_cast<const T *>(p.G), *U = static_cast<const T *>(p.U);
+    const T *dH = static_cast<const T *>(p.dH), *G = static_cast<const T *>(p.G);
+    const T *U = static_cast<const T *>(p.U);
     T *dG = static_cast<T *>(p.dG), *dU = static_cast<T *>(p.dU);
     const size_t n = (size_t)p.M * p.F, rows = (size_t)p.M * ((p.F + kSpan - 1) / kSpan);
     const size_t ctas = p.F % 8 ? rows : (n / 8 + kThreads - 1) / kThreads;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)ctas), block(kThreads);
-    if (p.F % 8 == 0) return launch_dependent(grad_act_kernel<T, ACT>, grid, block, 0, 1, stream, dH, G, U, dG, dU, n);
+    if (p.F % 8 == 0)
+        return launch_dependent(grad_act_kernel<T, ACT>, grid, block, 0, 1, stream, dH, G, U, dG, dU, n);
     if (p.F % 2 == 0)
-        return launch_dependent(grad_act_rows_kernel<T, ACT, true>, grid, block, 0, 1, stream, dH, G, U, dG, dU, p.F, p.Fp);
-    return launch_dependent(grad_act_rows_kernel<T, ACT, false>, grid, block, 0, 1, stream, dH, G, U, dG, dU, p.F, p.Fp);
+        return launch_dependent(grad_act_rows_kernel<T, ACT, true>, grid, block, 0, 1, stream, dH, G,
+                                U, dG, dU, p.F, p.Fp);
+    return launch_dependent(grad_act_rows_kernel<T, ACT, false>, grid, block, 0, 1, stream, dH, G, U,
+                            dG, dU, p.F, p.Fp);
 }
 
 } // namespace

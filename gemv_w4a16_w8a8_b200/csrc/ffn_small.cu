@@ -1,37 +1,37 @@
 // Few tokens: tensor-core kernel of the scaled W8A8 matmul, the gated forward products and dX.
 //
-// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns up to 128 tokens and R rows
-// of the weights (for kGated R / 2 of the gate and the same of up). R is any multiple of four, so that
-// the weights divide evenly over the SMs: tiles of 64 gate and up rows left 24 of 148 SMs with twice the
-// others' work at 11008 columns. The ring of 108 KB covers the memory's latency (44 GB/s x 2 us) and
-// leaves room for a second CTA: of this kernel, or of the next on the stream, which sets itself up
-// while this one ends.
+// Bound: HBM (every weight is read once, 2 M operations a byte). A CTA owns up to 128 tokens and R
+// rows of the weights (for kGated R / 2 of the gate and the same of up). R is any multiple of four,
+// so that the weights divide evenly over the SMs: tiles of 64 gate and up rows left 24 of 148 SMs
+// with twice the others' work at 11008 columns. The ring of 108 KB covers the memory's latency (44
+// GB/s x 2 us) and leaves room for a second CTA: of this kernel, or of the next on the stream,
+// which sets itself up while this one ends.
 //
-// Orientation (WM): up to 64 tokens the weights are the MMA's M side, in one or two blocks of 128, and
-// the tokens its N side; above, the tokens are the M side and the weights the N side. Unused rows of the
-// M side hold whatever follows in shared memory and reach no result, but the tensor core multiplies them:
-// with 16 tokens in an M of 128 the SMs drew enough power to fall from 1.8 to 1.45 GHz within a tenth of
-// a second, and the stream of weights slowed from 32.4 to 36 us with them. An MMA takes about 100 cycles for
-// up to 128 rows of 32 bytes by up to 128, 128 cycles by 256: 40 to 64 B of weights a clock, against the
-// 24 B that HBM delivers to an SM.
+// Orientation (WM): up to 64 tokens the weights are the MMA's M side, in one or two blocks of 128,
+// and the tokens its N side; above, the tokens are the M side and the weights the N side. Unused
+// rows of the M side hold whatever follows in shared memory and reach no result, but the tensor
+// core multiplies them: with 16 tokens in an M of 128 the SMs drew enough power to fall from 1.8 to
+// 1.45 GHz within a tenth of a second, and the stream of weights slowed from 32.4 to 36 us with
+// them. An MMA takes about 100 cycles for up to 128 rows of 32 bytes by up to 128, 128 cycles by
+// 256: 40 to 64 B of weights a clock, against the 24 B that HBM delivers to an SM.
 //
 // Split reduction: the CTAs of a cluster (1, 2, 4 or 8) take consecutive parts of the reduction of
 // one tile, so that a small weight matrix still occupies the device. Each leaves its partial tile
-// in its own shared memory as [token][weight row]; after a cluster barrier every CTA adds its share of
-// the columns over the cluster (distributed shared memory, parts in order: the same bits every run),
-// applies scales, bias or activation and writes runs of columns of one token. No workspace, no
-// atomics, one launch.
+// in its own shared memory as [token][weight row]; after a cluster barrier every CTA adds its share
+// of the columns over the cluster (distributed shared memory, parts in order: the same bits every
+// run), applies scales, bias or activation and writes runs of columns of one token. No workspace,
+// no atomics, one launch.
 //
-// Device time of calls that follow one another, weights not in L2: one token, 4096 x 11008 int8, 11.0 us
-// (45 MB, 4.1 TB/s); gate and up 11008 x 4096 int8, 17.1 us (90 MB, 5.3 TB/s); 16 tokens in 16 bits, 30.6 us
-// (181 MB, 5.9 TB/s); 32 tokens, 32000 x 4096, 24.7 us (133 MB, 5.4 TB/s); 16384 x 16384, 41.8 us (268 MB,
-// 6.4 TB/s). Of each about 3.5 us pass before the first slab arrives and after the last.
+// Device time of calls that follow one another, weights not in L2: one token, 4096 x 11008 int8,
+// 11.0 us (45 MB, 4.1 TB/s); gate and up 11008 x 4096 int8, 17.1 us (90 MB, 5.3 TB/s); 16 tokens in
+// 16 bits, 30.6 us (181 MB, 5.9 TB/s); 32 tokens, 32000 x 4096, 24.7 us (133 MB, 5.4 TB/s); 16384 x
+// 16384, 41.8 us (268 MB, 6.4 TB/s). Of each about 3.5 us pass before the first slab arrives and
+// after the last.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
 
-#include "ffn.cuh"
-#include "sm100.cuh"
+#include "ffn_mma.cuh"
 
 namespace qg {
 namespace {
@@ -46,7 +46,8 @@ constexpr int kRingBytes = 108 * 1024;
 constexpr int kMaxStages = 16;
 
 // after the ring: 8 rows that no copy fills, token scales, barriers, TMEM address and abort flag
-constexpr int kScaleOff = kRingBytes + 8 * kSlab, kBarOff = kScaleOff + kTokens * 4, kBars = 2 * kMaxStages + 1;
+constexpr int kScaleOff = kRingBytes + 8 * kSlab, kBarOff = kScaleOff + kTokens * 4;
+constexpr int kBars = 2 * kMaxStages + 1;
 constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 
@@ -68,29 +69,6 @@ struct Out {
     const float *sa, *sw, *sw1;
     const void *bias;
 };
-
-template <bool I8>
-__device__ __forceinline__ void mma_one(uint32_t dtm, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate)
-{
-    if constexpr (I8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtm),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtm),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                     : "memory");
-}
-
-template <bool I8, typename T, bool AMN, bool BMN> __device__ __forceinline__ uint32_t instr_desc(int n)
-{
-    constexpr uint32_t in = I8 ? 1u : (std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
-    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (AMN ? 1u : 0u) << 15 | (BMN ? 1u : 0u) << 16 |
-           (uint32_t)(n >> 3) << 17 | (uint32_t)(kMmaM >> 4) << 24;
-}
 
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr)
 {
@@ -126,18 +104,20 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     constexpr int kElems = I8 ? 128 : 64;
     const int ST = shape.stages, N = shape.N;
     const int x_bytes = shape.box_tokens * kSlab, w_bytes = shape.slab_rows * kSlab;
-    // the MMA's N, and accumulator columns: of each block of 128 weight rows (WM), or of the weights
+    // the MMA's N, and accumulator columns: of each block of 128 weight rows (WM), or of the
+    // weights
     const int mma_n = ((WM ? shape.box_tokens : shape.used) + 15) / 16 * 16;
     const int blocks = WM ? (shape.used + kMmaM - 1) / kMmaM : 1;
     const int acc_cols = mma_n * blocks;
-    const uint32_t cols_alloc = acc_cols <= 32 ? 32u : (acc_cols <= 64 ? 64u : (acc_cols <= 128 ? 128u : 256u));
+    uint32_t cols_alloc = 32;                      // a power of two
+    while ((int)cols_alloc < acc_cols) cols_alloc *= 2;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    // The slabs of the M side first: the MMA reads whole blocks of 128 rows from the start of one, which
-    // reach into later slabs and into the N side's; the N side's last slab, 8 rows at most, into the
-    // rows behind the ring.
+    // The slabs of the M side first: the MMA reads whole blocks of 128 rows from the start of one,
+    // which reach into later slabs and into the N side's; the N side's last slab, 8 rows at most,
+    // into the rows behind the ring.
     const uint32_t ring_m = smem_u32(base), ring_n = ring_m + ST * (WM ? w_bytes : x_bytes);
     const uint32_t ring_w = WM ? ring_m : ring_n, ring_x = WM ? ring_n : ring_m;
     float *scale_s = reinterpret_cast<float *>(base + kScaleOff);
@@ -181,7 +161,8 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         const bool second = FORM == kDx && s0 + i >= shape.seg_slabs;
         const int k = (s0 + i - (second ? shape.seg_slabs : 0)) * kElems;
         if constexpr (FORM == kDx) {
-            for (int c = 0; c < shape.used; c += 64) copy(c * kSlab, second ? &tm_w1 : &tm_w0, n0 + c, k);
+            for (int c = 0; c < shape.used; c += 64)
+                copy(c * kSlab, second ? &tm_w1 : &tm_w0, n0 + c, k);
         } else {
             copy(0, &tm_w0, k, n0);
             if constexpr (FORM == kGated) copy(shape.second * kSlab, &tm_w1, k, n0);
@@ -202,14 +183,16 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     const uint32_t tmem_base = *tmem_holder;
     grid_wait();
 
-    // This CTA's share of the tile, in groups of four columns: some of the tokens where there are enough
-    // of them (whole rows, the longest runs), else some of the groups. A thread keeps one group, whose
-    // factors it loads now, under the weights' stream, and takes every `step`-th token.
+    // This CTA's share of the tile, in groups of four columns: some of the tokens where there are
+    // enough of them (whole rows, the longest runs), else some of the groups. A thread keeps one
+    // group, whose factors it loads now, under the weights' stream, and takes every `step`-th
+    // token.
     const int groups = shape.cols / 4;
     const bool by_token = tokens >= 2 * cl;
     const int g0 = by_token ? 0 : groups * rank / cl;
     const int ng = by_token ? groups : groups * (rank + 1) / cl - g0;
-    const int token0 = by_token ? tokens * rank / cl : 0, token1 = by_token ? tokens * (rank + 1) / cl : tokens;
+    const int token0 = by_token ? tokens * rank / cl : 0;
+    const int token1 = by_token ? tokens * (rank + 1) / cl : tokens;
     const int step = ng > 0 ? kOutThreads / ng : 1;
     const int n = n0 + 4 * (g0 + (ng > 0 ? (int)threadIdx.x % ng : 0));
     const int first = token0 + (ng > 0 ? (int)threadIdx.x / ng : 0);
@@ -261,8 +244,8 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         }
     } else if (warp == 5) {
         // ---------------- MMA issue ----------------
-        const uint32_t idesc = instr_desc<I8, T, WM && WMN, !WM && WMN>(mma_n);
-        constexpr int kw = WMN ? 128 : 2;          // 16 rows of an MN-major slab, or 32 bytes of a K-major one
+        const uint32_t idesc = ffn_instr_desc<I8, T, WM && WMN, !WM && WMN>(kMmaM, mma_n);
+        constexpr int kw = WMN ? 128 : 2;      // 16 rows of an MN-major slab, 32 bytes of the other
         int s = 0;
         uint32_t phase = 0;
         for (int it = 0; it < ns; ++it) {
@@ -276,11 +259,13 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t accumulate = (it | k) != 0 ? 1u : 0u;
                     if constexpr (WM) {
-                        mma_one<I8>(tmem_base, dw + kw * k, dx + 2 * k, idesc, accumulate);
+                        ffn_mma<I8>(tmem_base, dw + kw * k, dx + 2 * k, idesc, accumulate);
                         // the next 128 rows: 16 KB on, in either layout
-                        if (blocks > 1) mma_one<I8>(tmem_base + mma_n, dw + kw * k + 1024, dx + 2 * k, idesc, accumulate);
+                        if (blocks > 1)
+                            ffn_mma<I8>(tmem_base + mma_n, dw + kw * k + 1024, dx + 2 * k, idesc,
+                                        accumulate);
                     } else {
-                        mma_one<I8>(tmem_base, dx + 2 * k, dw + kw * k, idesc, accumulate);
+                        ffn_mma<I8>(tmem_base, dx + 2 * k, dw + kw * k, idesc, accumulate);
                     }
                 }
                 mma_commit(empty_bar(s));
@@ -296,8 +281,9 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
         int dummy_abort = 0;
         mbar_wait(done_bar, 0, &dummy_abort, nullptr);
     }
-    // The accumulator to shared memory as [token][weight row]: lane = weight row (WM) or token. A CTA whose
-    // waits gave up has raised the error word; it goes through the same steps so that nobody hangs.
+    // The accumulator to shared memory as [token][weight row]: lane = weight row (WM) or token. A
+    // CTA whose waits gave up has raised the error word; it goes through the same steps so that
+    // nobody hangs.
     if (warp < 4) mbar_wait(done_bar, 0, abort_flag, err);
     __syncthreads();               // the copies have landed and the MMAs have read them
     uint32_t *part = reinterpret_cast<uint32_t *>(base);
@@ -327,18 +313,20 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (c + 4 * q < shape.used)
-                            *reinterpret_cast<uint4 *>(to + c + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            *reinterpret_cast<uint4 *>(to + c + 4 * q) =
+                                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             }
         }
         tc_fence_before();
     }
     __syncthreads();
-    // TMEM goes back before this CTA waits for others of its cluster: a kernel of another stream whose
-    // CTAs wait for it on one SM while theirs keep a CTA of this cluster waiting on another would
-    // otherwise never see it freed.
+    // TMEM goes back before this CTA waits for others of its cluster: a kernel of another stream
+    // whose CTAs wait for it on one SM while theirs keep a CTA of this cluster waiting on another
+    // would otherwise never see it freed.
     if (warp == 5) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(cols_alloc)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(cols_alloc)
                      : "memory");
     }
     if (cl > 1) cluster_sync();
@@ -413,20 +401,6 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 
 // ---- host side -------------------------------------------------------------------------------------
 
-struct Matrix {
-    const void *p;
-    uint64_t rows, cols, pitch;
-};
-
-template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, int box_rows)
-{
-    const CUtensorMapDataType dt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                      : (std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
-    return make_map(m, dt, x.p, x.cols, x.rows, x.pitch, I8 ? 128 : 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int round_up(int a, int b) { return ceil_div(a, b) * b; }
 
 // Stages of the ring: its bytes, and the whole blocks of 128 rows that the MMA reads from the last
@@ -446,21 +420,22 @@ struct Plan {
     double us;                // estimate for a B200
 };
 
-// Clusters of 1, 2, 4 and 8 CTAs that run at once on a B200 with one CTA an SM (larger clusters leave SMs
-// of a partly filled processing cluster idle) and with two.
+// Clusters of 1, 2, 4 and 8 CTAs that run at once on a B200 with one CTA an SM (larger clusters
+// leave SMs of a partly filled processing cluster idle) and with two.
 constexpr int kClusters[2][4] = {{148, 74, 33, 15}, {296, 148, 71, 33}};
 
-// Columns of a tile and parts of the reduction: for every cluster size and one or two CTAs an SM, the
-// columns that divide the weights evenly over the clusters that run at once (more waves of them if a
-// tile's columns would not fit), by the estimated time of
-//   - a slab: its MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together; more
-//     with a second block or a wide N side), what L2 delivers to an SM (115 GB/s), or the memory's 2 us
-//     over the slabs in flight;
+// Columns of a tile and parts of the reduction: for every cluster size and one or two CTAs an SM,
+// the columns that divide the weights evenly over the clusters that run at once (more waves of them
+// if a tile's columns would not fit), by the estimated time of
+//   - a slab: its MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together;
+//     more with a second block or a wide N side), what L2 delivers to an SM (115 GB/s), or the
+//     memory's 2 us over the slabs in flight;
 //   - the stream: the slabs of a CTA against HBM, the two slowing each other near balance;
 //   - joining: a barrier, and partial tiles through shared memory at 35 GB/s (60 GB/s unsplit).
-// Times in us of columns x parts, measured over a sweep: one token, 11008 gate and up columns, 4096 deep,
-// 76x2: 17.1, 76x1: 17.8, 40x1: 17.8, 64x1: 19.1, 128x1: 19.4; 16 tokens in 16 bits, 76x2: 30.6, 40x1:
-// 32.7, 64x1: 33.4, 76x1: 34.7; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5, 64x2: 10.6.
+// Times in us of columns x parts, measured over a sweep: one token, 11008 gate and up columns, 4096
+// deep, 76x2: 17.1, 76x1: 17.8, 40x1: 17.8, 64x1: 19.1, 128x1: 19.4; 16 tokens in 16 bits, 76x2:
+// 30.6, 40x1: 32.7, 64x1: 33.4, 76x1: 34.7; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5,
+// 64x2: 10.6.
 Plan plan_small(int form, int M, int N, int slabs)
 {
     const int tiles_t = ceil_div(M, kTokens), box = round_up(std::min(M, kTokens), 8);
@@ -483,11 +458,13 @@ Plan plan_small(int form, int M, int N, int slabs)
             const long long ctas = (long long)ceil_div(N, cols) * tiles_t * parts;
             const double on_sm = std::max(1.0, std::min(2.0, std::ceil(ctas / 148.0)));
             const double rounds = std::max(1.0, ctas / ((double)kClusters[1][i] * parts));
-            const int used = form == kGated ? round_up(cols, 8) + cols : cols, tokens = std::min(M, kTokens);
+            const int used = form == kGated ? round_up(cols, 8) + cols : cols;
+            const int tokens = std::min(M, kTokens);
             const int blocks = M <= kWeightMajor ? ceil_div(used, kMmaM) : 1;
             const double mma = on_sm < 2 ? (blocks > 1 ? 0.40 : (used > 128 ? 0.35 : 0.29))
                                          : (blocks > 1 ? 0.50 : 0.40 * std::max(1.0, used / 170.0));
-            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3, 2.0 / stages_of(used, box, M)});
+            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3,
+                                          2.0 / stages_of(used, box, M)});
             const double sm = ceil_div(slabs, parts) * slab * rounds;
             const double hbm = (double)slabs * kSlab * ((double)N * halves + M) / 6.4e6;
             const double stream = std::sqrt(std::sqrt(sm * sm * sm * sm + hbm * hbm * hbm * hbm));
@@ -511,7 +488,8 @@ cudaError_t launch_plan(const Matrix &w0, const Matrix &w1, const Matrix &x0, co
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!opted_in[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            const cudaError_t e =
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             if (e != cudaSuccess) return e;
             opted_in[dev] = true;
         }
@@ -531,20 +509,22 @@ cudaError_t launch_plan(const Matrix &w0, const Matrix &w1, const Matrix &x0, co
     // a slab's box: the tile's columns of a weight matrix, or 64 rows of the reduction for kDx
     CUtensorMap tw0, tw1, tx0, tx1;
     const int wbox = FORM == kDx ? 64 : plan.cols;
-    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tx0, x0, shape.box_tokens)) return cudaErrorInvalidValue;
+    if (!map_of<I8, T>(&tw0, w0, wbox) || !map_of<I8, T>(&tx0, x0, shape.box_tokens))
+        return cudaErrorInvalidValue;
     tw1 = tw0;
     tx1 = tx0;
     if (w1.p != w0.p && !map_of<I8, T>(&tw1, w1, wbox)) return cudaErrorInvalidValue;
     if (x1.p != x0.p && !map_of<I8, T>(&tx1, x1, shape.box_tokens)) return cudaErrorInvalidValue;
-    return launch_dependent(kern, dim3((unsigned)(tiles * plan.parts)), dim3(kThreads), kSmem, plan.parts, stream,
-                            tw0, tw1, tx0, tx1, shape, out, err);
+    return launch_dependent(kern, dim3((unsigned)(tiles * plan.parts)), dim3(kThreads), kSmem,
+                            plan.parts, stream, tw0, tw1, tx0, tx1, shape, out, err);
 }
 
 template <int FORM, bool I8, typename T>
 cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
                          const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
 {
-    if (shape.M <= kWeightMajor) return launch_plan<FORM, I8, T, true>(w0, w1, x0, x1, shape, out, err, stream);
+    if (shape.M <= kWeightMajor)
+        return launch_plan<FORM, I8, T, true>(w0, w1, x0, x1, shape, out, err, stream);
     return launch_plan<FORM, I8, T, false>(w0, w1, x0, x1, shape, out, err, stream);
 }
 
@@ -561,7 +541,11 @@ Shape shape_of(int M, int N, int seg_slabs, int segs, int act)
 
 } // namespace
 
-double small_us(int M, int N, bool gated, int slabs) { return plan_small(gated ? kGated : kScaled, M, N, slabs).us; }
+double small_us(int M, int N, bool gated, int slabs)
+{
+    return plan_small(gated ? kGated : kScaled, M, N, slabs).us;
+}
+
 double small_dx_us(int M, int F, int K) { return plan_small(kDx, M, K, 2 * ceil_div(F, 64)).us; }
 
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
@@ -580,7 +564,8 @@ cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaS
 cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K, pitch = K * 2;
-    const Matrix x{p.X, (uint64_t)p.M, K, pitch}, g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
+    const Matrix x{p.X, (uint64_t)p.M, K, pitch};
+    const Matrix g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
     const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr};
     const Shape shape = shape_of(p.M, p.F, ceil_div(p.K, 64), 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {

@@ -17,28 +17,27 @@
 //            makes gate and up of the same columns in one accumulator, and the epilogue of each
 //            token forms act(gate) * up
 //   kDx      dG Wg + dU Wu as one reduction over 2 F: the slabs of dG Wg, then those of dU Wu
-//   kDw      dG^T X and dU^T X: two results in one launch
-// Few tiles and a long reduction (kDx, kDw): the reduction is cut into parts that store fp32 partial
-// sums, added in order by a second kernel (no atomics: the same bits every run).
+//   kDw      dG^T X and dU^T X: two results in one launch Few tiles and a long reduction (kDx,
+// kDw): the reduction is cut into parts that store fp32 partial sums, added in order by a second
+// kernel (no atomics: the same bits every run).
 //
 // Warps: 0-7 epilogue (two for each quarter of the TMEM lanes, every other 32 columns each), 8 TMA
 // producer, 9 MMA issue (the pair's first CTA issues for both) and TMEM. Accumulators are double
 // buffered, so the epilogue of a tile runs under the next tile's MMAs. Every wait is bounded as in
 // the other tensor-core kernels.
 //
-// Bound: the tensor pipe. A tile of 256 columns asks an SM for 32 KB of operands per slab of 512 MMA
-// cycles, about what L2 delivers to one (90 GB/s), so it reaches 75 to 80 % of the MMA's rate with int8
-// and 80 to 92 % with 16 bits inside a wave. Device time of calls that follow one another: 8192 x 11008
-// x 4096 bf16, G and U saved, 0.99 ms cool (1.5 PFLOP/s, 92 % of the burst matmul rate) and 1.2 ms under
-// the power cap (88 % of the sustained rate); its backward pass 2.0 and 2.5 ms; int8 16384^3 2.7 ms (3.2
-// POP/s) and 3.3 ms; int8 512 x 11008 x 4096 gated 41 us. Weights fetched into L2 one ring ahead: 1 to
-// 20 % slower. A tile's epilogue takes about 2.5 us and bounds reductions shorter than 8 slabs
-// (16384 x 4096 x 256 int8: 47 us, 3.0 TB/s).
+// Bound: the tensor pipe. A tile of 256 columns asks an SM for 32 KB of operands per slab of 512
+// MMA cycles, about what L2 delivers to one (90 GB/s), so it reaches 75 to 80 % of the MMA's rate
+// with int8 and 80 to 92 % with 16 bits inside a wave. Device time of calls that follow one
+// another: 8192 x 11008 x 4096 bf16, G and U saved, 0.99 ms cool (1.5 PFLOP/s, 92 % of the burst
+// matmul rate) and 1.2 ms under the power cap (88 % of the sustained rate); its backward pass 2.0
+// and 2.5 ms; int8 16384^3 2.7 ms (3.2 POP/s) and 3.3 ms; int8 512 x 11008 x 4096 gated 41 us.
+// Weights fetched into L2 one ring ahead: 1 to 20 % slower. A tile's epilogue takes about 2.5 us
+// and bounds reductions shorter than 8 slabs (16384 x 4096 x 256 int8: 47 us, 3.0 TB/s).
 #include <algorithm>
 #include <mutex>
 
-#include "ffn.cuh"
-#include "sm100.cuh"
+#include "ffn_mma.cuh"
 
 namespace qg {
 namespace {
@@ -50,10 +49,10 @@ constexpr int kThreads = 32 * (kEpiWarps + 2);
 constexpr int kTileM = 256, kRows = 128;       // rows of the result: of a pair, of a CTA
 constexpr int kMaxBn = 256;
 constexpr int kSlab = 128;                     // bytes of the reduction per stage (K-major)
-constexpr int kRasterM = 8;                    // row tiles per raster group (4, 16: the same within noise)
+constexpr int kRasterM = 8;                    // row tiles per raster group (4, 16: no faster)
 
-// Shared memory: stages of a CTA's 128 rows x 128 B and up to 128 rows x 128 B of the other operand,
-// then for each epilogue warp 32 rows x 64 B of results and 64 column factors.
+// Shared memory: stages of a CTA's 128 rows x 128 B and up to 128 rows x 128 B of the other
+// operand, then for each epilogue warp 32 rows x 64 B of results and 64 column factors.
 namespace ring {
 constexpr int a_bytes = kRows * kSlab;
 constexpr int stage = a_bytes + kMaxBn / 2 * kSlab;
@@ -109,33 +108,8 @@ __device__ __forceinline__ Unit unit_of(int u, const Shape &s, int ncol)
     return w;
 }
 
-template <bool I8>
-__device__ __forceinline__ void mma_pair(uint32_t dtm, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate)
-{
-    if constexpr (I8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtm),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtm),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-                     : "memory");
-}
-
-// int8: s32 accumulator (2), signed operands (1). 16-bit: fp32 accumulator (1), fp16 (0) or bf16
-// (1) operands; bits 15 and 16: MN-major A and B.
-template <bool I8, typename T, bool AMN, bool BMN> __device__ __forceinline__ uint32_t instr_desc(int bn)
-{
-    constexpr uint32_t in = I8 ? 1u : (std::is_same<T, __nv_bfloat16>::value ? 1u : 0u);
-    return (I8 ? 2u : 1u) << 4 | in << 7 | in << 10 | (AMN ? 1u : 0u) << 15 | (BMN ? 1u : 0u) << 16 |
-           (uint32_t)(bn >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
-}
-
-// A warp's 32 rows x 64 bytes of results, staged in shared memory (16-byte piece j of row r at
-// j ^ (r / 2 & 3): neither side has bank conflicts) and written as whole rows: 16 bytes a lane where
+// A warp's 32 rows x 64 bytes of results, staged in shared memory (16-byte piece j of row r at j ^
+// (r / 2 & 3): neither side has bank conflicts) and written as whole rows: 16 bytes a lane where
 // rows of the result are 16-byte aligned, else a row at a time, an element a lane.
 __device__ __forceinline__ void stage_put(uint8_t *stage, int lane, const uint32_t (&x)[16])
 {
@@ -156,13 +130,14 @@ __device__ __forceinline__ void stage_flush(const uint8_t *stage, E *c, size_t l
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + (lane >> 2);
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
+            const uint4 v =
+                *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ (r >> 1 & 3)) << 4));
             if (r < rows && j * kPer < cols)
                 *reinterpret_cast<uint4 *>(c + (size_t)r * ld + j * kPer) = v;
         }
     } else {
-        // 4-byte elements fill half a warp's lanes: two rows an instruction. Eight loads, then their
-        // stores, from a pointer that moves down the rows.
+        // 4-byte elements fill half a warp's lanes: two rows an instruction. Eight loads, then
+        // their stores, from a pointer that moves down the rows.
         constexpr int kAt = 32 / kCols, kBatch = 8;
         const int q = lane % kCols, r0 = lane / kCols;
         const uint8_t *from = stage + r0 * 64 + (q % kPer) * sizeof(E);
@@ -175,7 +150,8 @@ __device__ __forceinline__ void stage_flush(const uint8_t *stage, E *c, size_t l
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int at = r + i * kAt;
-                v[i] = *reinterpret_cast<const E *>(from + (at - r0) * 64 + (((q / kPer) ^ (at >> 1 & 3)) << 4));
+                v[i] = *reinterpret_cast<const E *>(from + (at - r0) * 64 +
+                                                    (((q / kPer) ^ (at >> 1 & 3)) << 4));
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -319,7 +295,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         }
     } else if (warp == kMmaWarp && rank == 0) {
         // ---------------- MMA issue for both CTAs ----------------
-        const uint32_t idesc = instr_desc<I8, T, AMN, BMN>(bn);
+        const uint32_t idesc = ffn_instr_desc<I8, T, AMN, BMN>(kTileM, bn);
         int s = 0, j = 0;
         uint32_t phase = 0;
         bool stop = false;
@@ -343,7 +319,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                 if (lane == 0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_pair<I8>(dtm, da + ka * k, db + kb * k, idesc, (i | k) != 0 ? 1u : 0u);
+                        ffn_mma_pair<I8>(dtm, da + ka * k, db + kb * k, idesc, (i | k) != 0 ? 1u : 0u);
                     mma_commit_pair_both(empty_bar(s));
                 }
                 __syncwarp();
@@ -368,8 +344,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         const int quarter = warp & 3, first = 32 * (warp >> 2);
         const int N = shape.N;
         const bool vec = (N & 7) == 0;
-        // A lane's row scale, and the factors of column c + lane of a tile: the two scales of kGated, or
-        // scale and bias. A tile's first ones are loaded while the tile before it is written.
+        // A lane's row scale, and the factors of column c + lane of a tile: the two scales of
+        // kGated, or scale and bias. A tile's first ones are loaded while the tile before it is
+        // written.
         float sa = 0.f, f0 = 0.f, f1 = 0.f;
         auto factors = [&](const Unit &w, int c) {
             const int n = min(w.n0 + min(c + lane, ncol - 1), N - 1);
@@ -423,10 +400,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                         stage_put(stage, lane, x);
                         if (vec || (N & 1)) stage_flush(stage, dst, N, rows, cols, lane, vec);
                         else     // pairs of elements
-                            stage_flush(stage, reinterpret_cast<uint32_t *>(dst), N / 2, rows, cols / 2, lane, false);
+                            stage_flush(stage, reinterpret_cast<uint32_t *>(dst), N / 2, rows,
+                                        cols / 2, lane, false);
                     };
-                    // int32 sums to fp32, scaled by their row and then their column, as the definition
-                    // has it; then the bias
+                    // int32 sums to fp32, scaled by their row and then their column, as the
+                    // definition has it; then the bias
                     if constexpr (I8) {
                         auto scale = [&](uint32_t (&x)[32], int at) {
 #pragma unroll
@@ -435,8 +413,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                                 const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    x[4 * q + e] = __float_as_uint(
-                                        __fmul_rn(__fmul_rn(__int2float_rn((int)x[4 * q + e]), sa), fs[e]));
+                                    x[4 * q + e] = __float_as_uint(__fmul_rn(
+                                        __fmul_rn(__int2float_rn((int)x[4 * q + e]), sa), fs[e]));
                             }
                         };
                         scale(v, 0);
@@ -449,7 +427,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                                 const float fs[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    v[4 * q + e] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * q + e]), fs[e]));
+                                    v[4 * q + e] = __float_as_uint(
+                                        __fadd_rn(__uint_as_float(v[4 * q + e]), fs[e]));
                             }
                         }
                     }
@@ -460,11 +439,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                             constexpr int ACT = decltype(act)::value;
 #pragma unroll
                             for (int q = 0; q < 16; ++q) {
-                                const float g[2] = {__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])};
-                                const float x[2] = {__uint_as_float(z[2 * q]), __uint_as_float(z[2 * q + 1])};
-                                hw[q] = pack2<T>(act_value<ACT>(g[0]) * x[0], act_value<ACT>(g[1]) * x[1]);
-                                gw[q] = pack2<T>(g[0], g[1]);
-                                uw[q] = pack2<T>(x[0], x[1]);
+                                const float g0 = __uint_as_float(v[2 * q]);
+                                const float g1 = __uint_as_float(v[2 * q + 1]);
+                                const float u0 = __uint_as_float(z[2 * q]);
+                                const float u1 = __uint_as_float(z[2 * q + 1]);
+                                hw[q] = pack2<T>(act_value<ACT>(g0) * u0, act_value<ACT>(g1) * u1);
+                                gw[q] = pack2<T>(g0, g1);
+                                uw[q] = pack2<T>(u0, u1);
                             }
                         };
                         if (shape.act == QG_ACT_SILU) gate(Const<QG_ACT_SILU>{});
@@ -478,7 +459,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                             }
                         }
                     } else if (FORM != kScaled && shape.parts > 1) {
-                        float *dst = out.part + ((size_t)(w.which * shape.parts + w.part) * shape.M + m) * N + w.n0 + c;
+                        const size_t row = (size_t)(w.which * shape.parts + w.part) * shape.M + m;
+                        float *dst = out.part + row * N + w.n0 + c;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -496,8 +478,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                 }
             }
             else if constexpr (I8) factors(next, first);
-            // The accumulator goes back to the MMA warp (of the pair's first CTA). All that this orders
-            // are reads of TMEM that have returned; a release would wait for the results' stores.
+            // The accumulator goes back to the MMA warp (of the pair's first CTA). All that this
+            // orders are reads of TMEM that have returned; a release would wait for the results'
+            // stores.
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(acce_bar(b), 0));
@@ -509,26 +492,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     cluster_sync();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kCols)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(kCols)
                      : "memory");
     }
 }
 
 // ---- host side -------------------------------------------------------------------------------------
-
-struct Matrix {          // a 16-bit or int8 matrix [rows, cols] with `pitch` bytes a row
-    const void *p;
-    uint64_t rows, cols, pitch;
-};
-
-template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, bool mn, int box_rows)
-{
-    const CUtensorMapDataType dt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                      : (std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
-    return make_map(m, dt, x.p, x.cols, x.rows, x.pitch, I8 ? 128 : 64, mn ? 64 : box_rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
-}
 
 template <int FORM, bool I8, typename T>
 cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, const Matrix &b1,
@@ -544,7 +514,8 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!pairs_of[dev]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring::total);
+            cudaError_t e = cudaFuncSetAttribute(
+                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring::total);
             if (e != cudaSuccess) return e;
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[1];
@@ -567,17 +538,17 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
     }
     if (shape.units <= 0) return cudaErrorInvalidValue;        // more tiles than an int counts
     CUtensorMap ta0, ta1, tb0, tb1;
-    if (!map_of<I8, T>(&ta0, a0, AMN, kRows) || !map_of<I8, T>(&tb0, b0, BMN, shape.bn / 2))
+    // MN-major operands arrive in boxes of 64 rows of the reduction
+    const int a_rows = AMN ? 64 : kRows, b_rows = BMN ? 64 : shape.bn / 2;
+    if (!map_of<I8, T>(&ta0, a0, a_rows) || !map_of<I8, T>(&tb0, b0, b_rows))
         return cudaErrorInvalidValue;
     ta1 = ta0;
     tb1 = tb0;
-    if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, AMN, kRows)) return cudaErrorInvalidValue;
-    if (b1.p != b0.p && !map_of<I8, T>(&tb1, b1, BMN, shape.bn / 2)) return cudaErrorInvalidValue;
-    return launch_dependent(kern, dim3(2 * std::min(shape.units, pairs)), dim3(kThreads), ring::total, 2, stream,
-                            ta0, ta1, tb0, tb1, shape, out, err);
+    if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, a_rows)) return cudaErrorInvalidValue;
+    if (b1.p != b0.p && !map_of<I8, T>(&tb1, b1, b_rows)) return cudaErrorInvalidValue;
+    return launch_dependent(kern, dim3(2 * std::min(shape.units, pairs)), dim3(kThreads),
+                            ring::total, 2, stream, ta0, ta1, tb0, tb1, shape, out, err);
 }
-
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Widths that the MMA of a pair takes: multiples of 32 for int8 and of 16 for 16-bit types; for
 // MN-major operands whole chunks of 64 values in each CTA.
@@ -591,12 +562,12 @@ struct Plan {
 };
 
 // Tile width and parts of the reduction with the shortest schedule: whole waves of units over the
-// CTA pairs. A slab takes 0.34 us in a wave that fills the device, nearly whatever the width:
-// 128 columns 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and
-// L2 delivers little more than 90 GB/s to an SM); so fewest waves win, and among them the narrower
-// tile, whose epilogue is shorter. 2 x 43 tiles of 256 columns on 74 pairs, say, leave most of a second
-// wave idle: 2 x 69 tiles of 160 take the same two waves 15 % faster (509 x 11007 x 4080: 38.3 ->
-// 32.4 us). Parts cost their fp32 sums' way to memory and back and a second kernel.
+// CTA pairs. A slab takes 0.34 us in a wave that fills the device, nearly whatever the width: 128
+// columns 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and L2
+// delivers little more than 90 GB/s to an SM); so fewest waves win, and among them the narrower
+// tile, whose epilogue is shorter. 2 x 43 tiles of 256 columns on 74 pairs, say, leave most of a
+// second wave idle: 2 x 69 tiles of 160 take the same two waves 15 % faster (509 x 11007 x 4080:
+// 38.3 -> 32.4 us). Parts cost their fp32 sums' way to memory and back and a second kernel.
 Plan plan_tiles(int M, int N, int results, bool gated, int step, int slabs, int max_parts)
 {
     const long tm = ceil_div(M, kTileM);
@@ -616,12 +587,19 @@ Plan plan_tiles(int M, int N, int results, bool gated, int step, int slabs, int 
     return best;
 }
 
-Plan plan_dx(int M, int F, int K) { return plan_tiles(M, K, 1, false, kStepMn, 2 * ceil_div(F, 64), kMaxParts); }
-Plan plan_dw(int M, int F, int K) { return plan_tiles(F, K, 2, false, kStepMn, ceil_div(M, 64), kMaxParts); }
+Plan plan_dx(int M, int F, int K)
+{
+    return plan_tiles(M, K, 1, false, kStepMn, 2 * ceil_div(F, 64), kMaxParts);
+}
+Plan plan_dw(int M, int F, int K)
+{
+    return plan_tiles(F, K, 2, false, kStepMn, ceil_div(M, 64), kMaxParts);
+}
 
 // Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n)
+__global__ void __launch_bounds__(256)
+join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n)
 {
     grid_release();
     grid_wait();
@@ -630,20 +608,24 @@ __global__ void __launch_bounds__(256) join_kernel(const float *__restrict__ par
     const float *src = part + (size_t)blockIdx.y * parts * n + at;
     float r[8] = {};
     for (int p = 0; p < parts; ++p, src += n) {
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        const float4 a = *reinterpret_cast<const float4 *>(src);
+        const float4 b = *reinterpret_cast<const float4 *>(src + 4);
         r[0] += a.x, r[1] += a.y, r[2] += a.z, r[3] += a.w;
         r[4] += b.x, r[5] += b.y, r[6] += b.z, r[7] += b.w;
     }
     *reinterpret_cast<uint4 *>((blockIdx.y ? c1 : c0) + at) =
-        make_uint4(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]), pack2<T>(r[4], r[5]), pack2<T>(r[6], r[7]));
+        make_uint4(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]), pack2<T>(r[4], r[5]),
+                   pack2<T>(r[6], r[7]));
 }
 
 template <typename T>
-cudaError_t join_parts(const float *part, void *c0, void *c1, const Shape &s, cudaStream_t stream)
+cudaError_t join_parts(const float *part, void *c0, void *c1, const Shape &s,
+                       cudaStream_t stream)
 {
     const long long n = (long long)s.M * s.N;
-    return launch_dependent(join_kernel<T>, dim3((unsigned)((n / 8 + 255) / 256), c1 ? 2 : 1), dim3(256), 0, 1, stream,
-                            part, static_cast<T *>(c0), static_cast<T *>(c1), s.parts, n);
+    const dim3 grid((unsigned)((n / 8 + 255) / 256), c1 ? 2 : 1);
+    return launch_dependent(join_kernel<T>, grid, dim3(256), 0, 1, stream, part,
+                            static_cast<T *>(c0), static_cast<T *>(c1), s.parts, n);
 }
 
 Shape shape_of(int M, int N, int bn, int ncol, int results, int seg_slabs, int segs, int parts, int act)
@@ -676,7 +658,8 @@ double tile_dx_us(int M, int F, int K) { return plan_dx(M, F, K).us; }
 size_t tile_grad_part_bytes(int M, int F, int K)
 {
     const Plan x = plan_dx(M, F, K), w = plan_dw(M, F, K);
-    const size_t nx = x.parts > 1 ? (size_t)x.parts * M * K : 0, nw = w.parts > 1 ? (size_t)w.parts * 2 * F * K : 0;
+    const size_t nx = x.parts > 1 ? (size_t)x.parts * M * K : 0;
+    const size_t nw = w.parts > 1 ? (size_t)w.parts * 2 * F * K : 0;
     return std::max(nx, nw) * 4;
 }
 
@@ -699,7 +682,8 @@ cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaSt
 cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const uint64_t K = p.K, pitch = K * 2;
-    const Matrix x{p.X, (uint64_t)p.M, K, pitch}, g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
+    const Matrix x{p.X, (uint64_t)p.M, K, pitch};
+    const Matrix g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
     const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr, nullptr};
     const int slabs = ceil_div(p.K, 64);
     const int bn = plan_tiles(p.M, p.F, 1, true, kStep16, slabs, 1).bn;

@@ -40,23 +40,27 @@ def quant(x):
     return q.astype(np.int8), scale.astype(np.float32)
 
 
+def _tanh_arg(g):
+    """2 sqrt(2/pi) (g + 0.044715 g^3): 0.5 (1 + tanh(x / 2)) is the logistic function of it."""
+    return 2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)
+
+
 def value(g, act):
+    """In forms without cancellation far below 0 (1 + erf and 1 + tanh lose everything there)."""
     if act == "silu":
         return g * torch.sigmoid(g)
     if act == "gelu":
-        return g * torch.special.ndtr(g)
-    return 0.5 * g * (1 + torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)))
+        return 0.5 * g * torch.special.erfc(-g / math.sqrt(2))
+    return g * torch.sigmoid(_tanh_arg(g))
 
 
 def slope(g, act):
     if act == "silu":
-        s = torch.sigmoid(g)
-        return s + g * s * (1 - s)
+        return torch.sigmoid(g) * (1 + g * torch.sigmoid(-g))
     if act == "gelu":
-        return torch.special.ndtr(g) + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
-    c = math.sqrt(2 / math.pi)
-    t = torch.tanh(c * (g + 0.044715 * g ** 3))
-    return 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+        return 0.5 * torch.special.erfc(-g / math.sqrt(2)) + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    x = _tanh_arg(g)
+    return torch.sigmoid(x) * (1 + g * torch.sigmoid(-x) * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * g * g))
 
 
 def rounded(ref, err, dtype):

@@ -278,6 +278,29 @@ def test_backward_parts_alone(act):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype", TYPES)
+def test_every_gate_value(act, dtype):
+    """The activation and its derivative at every 16-bit number up to 100 in size: with dH = U = X = 1
+    the weights' gradients are act'(G) and act(G), rounded twice (the second time exactly). Bound:
+    2^-18 relative, the exponential's argument (|x| <= 2 |g| (1 + g^2 / 20) where the result is above
+    2^-110, so |x| <= 80) by 2^-23 each way, and for a derivative, whose terms may cancel, 2^-22 of
+    the larger term."""
+    g = torch.arange(-32768, 32768, device=DEV, dtype=torch.int32).to(torch.int16).view(dtype)
+    g = g[torch.isfinite(g) & (g.abs() <= 100)]
+    F = g.numel()
+    g = g.view(1, F)
+    one, zero = torch.ones(1, F, device=DEV, dtype=dtype), torch.zeros(F, 8, device=DEV, dtype=dtype)
+    X = torch.ones(1, 8, device=DEV, dtype=dtype)
+    _, dWg, dWu = qg.qgemm_dense_gated_backward(one, X, zero, zero, g, one, act=act, need_dx=False)
+    x = g[0].double()
+    arg = torch.where(x < 0, 80 * 2.0 ** -22, 2.0 ** -22)
+    v, d = R.value(x, act), R.slope(x, act)
+    tail = torch.sigmoid(2.6 * x) * (1 + x.abs()) ** 3       # of the size of the derivative's terms
+    R.check(dWu[:, 0], (v, R.rounded(v, v.abs() * (2.0 ** -18 + arg) + 2.0 ** -110, dtype)), "value")
+    R.check(dWg[:, 0], (d, R.rounded(d, (d.abs() + tail) * (2.0 ** -18 + arg) + 2.0 ** -110, dtype)), "slope")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", TYPES)
 def test_backward_against_differences(act, dtype):
     """Directional differences of the 64-bit forward pass, G and U saved by the library's. The
     bound: the elementwise bounds of the gradients along the direction, what rounding G and U
