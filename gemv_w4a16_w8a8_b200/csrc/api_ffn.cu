@@ -105,7 +105,7 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
 size_t qgemm_dense_gated_backward_workspace_bytes(int M, int F, int K)
 {
     if (M <= 0 || F <= 0 || K <= 0 || K % 8) return 0;
-    return 2 * grad_bytes(M, F) + round256(tile_grad_part_bytes(M, F, K));
+    return 2 * grad_bytes(M, F) + round256(gated_backward_part_bytes(M, F, K));
 }
 
 qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,

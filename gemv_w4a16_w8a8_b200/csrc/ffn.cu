@@ -98,7 +98,20 @@ template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cuda
                             dG, dU, p.F, p.Fp);
 }
 
+// Whether dX goes to the few-token kernel, and only the weights' gradients to the tiles, or all of
+// them to one launch of tiles. By the sizes alone, not by what is asked for.
+bool dx_by_few(int M, int F, int K)
+{
+    return M <= kFewTokens ||
+           small_dx_us(M, F, K) + tile_grad_us(M, F, K, false) < tile_grad_us(M, F, K, true);
+}
+
 } // namespace
+
+size_t gated_backward_part_bytes(int M, int F, int K)
+{
+    return tile_grad_part_bytes(M, F, K, !dx_by_few(M, F, K));
+}
 
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
@@ -125,11 +138,9 @@ cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStr
             e = run_grad_act<T, ACT>(p, stream);
         });
     });
-    if (e == cudaSuccess && p.dX) {
-        const bool few = p.M <= kFewTokens || small_dx_us(p.M, p.F, p.K) < tile_dx_us(p.M, p.F, p.K);
-        e = few ? launch_small_dx(p, err, stream) : launch_tile_dx(p, err, stream);
-    }
-    if (e == cudaSuccess && p.dWg) e = launch_tile_dw(p, err, stream);
+    const bool few = dx_by_few(p.M, p.F, p.K);
+    if (e == cudaSuccess && few && p.dX) e = launch_small_dx(p, err, stream);
+    if (e == cudaSuccess) e = launch_tile_grad(p, !few, err, stream);
     return e;
 }
 

@@ -166,7 +166,7 @@ struct GatedGrad {          // backward; dG, dU and part live in the caller's wo
     void *dX, *dWg, *dWu, *dG, *dU;
     int M, F, K, act, dtype;
     int Fp;                 // row pitch of dG and dU in elements (a multiple of 8)
-    float *part;            // partial sums, tile_grad_part_bytes() bytes
+    float *part;            // partial sums, gated_backward_part_bytes() bytes
 };
 
 cudaError_t launch_quant_int8_tokens(const void *X, int8_t *Q, float *scales, int M, int K,
@@ -174,16 +174,18 @@ cudaError_t launch_quant_int8_tokens(const void *X, int8_t *Q, float *scales, in
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_dense_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
+// bytes of GatedGrad::part
+size_t gated_backward_part_bytes(int M, int F, int K);
 
 // Large tiles (ffn_tile.cu) and few tokens (ffn_small.cu): each takes any sizes. The estimates, in
 // microseconds, choose between them; slabs: 128-byte steps of the reduction.
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
-cudaError_t launch_tile_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
-cudaError_t launch_tile_dw(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
+cudaError_t launch_tile_grad(const GatedGrad &p, bool with_dx, unsigned int *err,
+                             cudaStream_t stream);
 double tile_us(int M, int N, bool gated, bool i8, int slabs);
-double tile_dx_us(int M, int F, int K);
-size_t tile_grad_part_bytes(int M, int F, int K);
+double tile_grad_us(int M, int F, int K, bool with_dx);
+size_t tile_grad_part_bytes(int M, int F, int K, bool with_dx);
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream);

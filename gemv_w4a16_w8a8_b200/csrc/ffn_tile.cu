@@ -17,9 +17,14 @@
 //            makes gate and up of the same columns in one accumulator, and the epilogue of each
 //            token forms act(gate) * up
 //   kDx      dG Wg + dU Wu as one reduction over 2 F: the slabs of dG Wg, then those of dU Wu
-//   kDw      dG^T X and dU^T X: two results in one launch Few tiles and a long reduction (kDx,
-// kDw): the reduction is cut into parts that store fp32 partial sums, added in order by a second
-// kernel (no atomics: the same bits every run).
+//   kDw      dG^T X and dU^T X: two results in one launch
+//   kBoth    kDx and kDw in one launch. dX's tiles are few and long, the weights' many and short: the
+//            pairs that get one tile of dX less than others take as many of the weights' tiles for
+//            it, then all share the rest, so that both products end together instead of leaving
+//            a partial wave each (3000 x 1500 x 700: 52 -> 37 us). Its slabs are 3 to 8 % slower
+//            (operand layouts are chosen unit by unit), so whole waves stay with two launches
+// Few tiles and a long reduction (gradients): the reduction is cut into parts that store fp32 partial
+// sums, added in order by a second kernel (no atomics: the same bits every run).
 //
 // Warps: 0-7 epilogue (two for each quarter of the TMEM lanes, every other 32 columns each), 8 TMA
 // producer, 9 MMA issue (the pair's first CTA issues for both) and TMEM. Accumulators are double
@@ -42,7 +47,9 @@
 namespace qg {
 namespace {
 
-enum Form { kScaled, kGated, kDx, kDw };
+enum Form { kScaled, kGated, kDx, kDw, kBoth };
+
+constexpr bool is_grad(int form) { return form >= kDx; }
 
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
@@ -65,20 +72,27 @@ constexpr int total = 1024 + bar_off + nbars * 8 + 16;
 static_assert(total <= 227 * 1024, "shared memory");
 } // namespace ring
 
-struct Shape {
-    int M, N;               // the result's rows and columns (N: columns of H for kGated)
-    int bn;                 // the MMA's N: columns of a tile (kGated: of gate and up together)
-    int tiles_m, tiles_n;
-    int seg_slabs;          // slabs of the reduction (of one of the two products for kDx)
-    int slabs;              // slabs in all: 2 seg_slabs for kDx
+// One product of a launch (gradients: dX, and the two weights' gradients together)
+struct Work {
+    int M, tiles_m;         // the result's rows, and tiles of them
+    int slabs;              // slabs of the reduction
     int parts, part_slabs;  // parts of the reduction and slabs of each (the last may have fewer)
-    int units;              // results x tiles x parts
+    int units;              // results x tiles x parts; 0: not computed
+};
+
+struct Shape {
+    int N, tiles_n;         // the result's columns (of H for kGated)
+    int bn;                 // the MMA's N: columns of a tile (kGated: of gate and up together)
+    int seg_slabs;          // slabs of one of dX's two products
     int act;
+    Work x, w;              // the product, or dX; the weights' gradients
+    int full, rem;          // units of x: `full` a pair, one more for the first `rem` pairs
+    int extra;              // tiles of w that pairs with one tile of x less take for it
 };
 
 struct Out {
-    void *c0, *c1, *c2;                 // C / H, G, U / dX / dWg, dWu
-    float *part;                        // fp32 partial sums [result][part][M][N]
+    void *c0, *c1, *c2;                 // C / H, G, U / dX, dWg, dWu
+    float *part_x, *part_w;             // fp32 partial sums [result][part][M][N]
     const float *sa, *sw, *sw1;
     const void *bias;
 };
@@ -89,23 +103,46 @@ struct Unit {
 
 // Tiles in groups of kRasterM row tiles, rows fastest: the pairs at work at one time share a block
 // of about kRasterM x 9 tiles whose operands stay in L2.
-__device__ __forceinline__ Unit unit_of(int u, const Shape &s, int ncol)
+__device__ __forceinline__ Unit unit_of(int u, const Work &k, int tiles_n, int ncol)
 {
     Unit w;
-    w.part = u % s.parts;
-    int t = u / s.parts;
-    const int per = s.tiles_m * s.tiles_n;
+    w.part = u % k.parts;
+    int t = u / k.parts;
+    const int per = k.tiles_m * tiles_n;
     w.which = t / per;
     t -= w.which * per;
-    const int group = t / (kRasterM * s.tiles_n);
+    const int group = t / (kRasterM * tiles_n);
     const int first = group * kRasterM;
-    const int gm = min(kRasterM, s.tiles_m - first);
-    t -= group * kRasterM * s.tiles_n;
+    const int gm = min(kRasterM, k.tiles_m - first);
+    t -= group * kRasterM * tiles_n;
     w.m0 = (first + t % gm) * kTileM;
     w.n0 = (t / gm) * ncol;
-    w.s0 = w.part * s.part_slabs;
-    w.ns = min(s.part_slabs, s.slabs - w.s0);
+    w.s0 = w.part * k.part_slabs;
+    w.ns = min(k.part_slabs, k.slabs - w.s0);
     return w;
+}
+
+// The j-th unit of this pair, in *w; false behind its last one.
+template <int FORM>
+__device__ __forceinline__ bool unit_at(int j, const Shape &s, int ncol, Unit *w)
+{
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int u = j * pairs + pair;
+    if (FORM != kDw && u < s.x.units) {
+        *w = unit_of(u, s.x, s.tiles_n, ncol);
+        return true;
+    }
+    if constexpr (FORM != kDw && FORM != kBoth) return false;
+    const int i = j - s.full - (pair < s.rem ? 1 : 0);
+    int v = i * pairs + pair;
+    if (s.rem > 0) {
+        if (pair >= s.rem && i < s.extra) v = i * (pairs - s.rem) + pair - s.rem;
+        else v += s.extra * (pairs - s.rem) - (pair >= s.rem ? s.extra * pairs : 0);
+    }
+    if (v >= s.w.units) return false;
+    *w = unit_of(v, s.w, s.tiles_n, ncol);
+    w->which += 1;
+    return true;
 }
 
 // A warp's 32 rows x 64 bytes of results, staged in shared memory (16-byte piece j of row r at j ^
@@ -167,9 +204,19 @@ template <int FORM, bool I8, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
             const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
-            const Shape shape, const Out out, unsigned int *err)
+            const __grid_constant__ CUtensorMap tm_a2, const __grid_constant__ CUtensorMap tm_a3,
+            const __grid_constant__ CUtensorMap tm_b2, const Shape shape, const Out out,
+            unsigned int *err)
 {
-    constexpr bool AMN = FORM == kDw, BMN = FORM == kDx || FORM == kDw;
+    // MN-major operands: B of every gradient, A of the weights' (kBoth: unit by unit, from the unit's
+    // place alone, so that the compiler sees one value for the warp: what depends on it goes into
+    // descriptors)
+    constexpr bool BMN = is_grad(FORM);
+    auto a_mn = [&](int j) {
+        if constexpr (FORM == kBoth)
+            return j * (int)(gridDim.x >> 1) + (int)(blockIdx.x >> 1) >= shape.x.units;
+        else return FORM == kDw;
+    };
     constexpr int kElems = I8 ? 128 : 64;                      // reduction values per slab
     constexpr uint32_t kCols = 2 * kMaxBn;
     constexpr int ST = ring::stages;
@@ -190,7 +237,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1;          // in the pair (known to be the same for the CTA)
-    const int ustart = blockIdx.x >> 1, ustep = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -219,11 +265,15 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     const uint32_t tmem_base = *tmem_holder;
     const uint32_t tx = ring::a_bytes + (BMN ? (half + 63) / 64 * 64 : half) * kSlab;
     // maps, first row of each operand, and place in the reduction of slab i of a unit
-    auto second = [&](const Unit &w, int i) { return FORM == kDx && w.s0 + i >= shape.seg_slabs; };
+    auto second = [&](const Unit &w, int i) {
+        return (FORM == kDx || (FORM == kBoth && w.which == 0)) && w.s0 + i >= shape.seg_slabs;
+    };
     auto map_a = [&](const Unit &w, int i) {
-        return (FORM == kDw ? w.which != 0 : second(w, i)) ? &tm_a1 : &tm_a0;
+        if (FORM == kDw || (FORM == kBoth && w.which)) return w.which == 2 ? &tm_a3 : &tm_a2;
+        return second(w, i) ? &tm_a1 : &tm_a0;
     };
     auto map_b = [&](const Unit &w, int i) {
+        if (FORM == kDw || (FORM == kBoth && w.which)) return &tm_b2;
         return (FORM == kGated ? rank != 0 : second(w, i)) ? &tm_b1 : &tm_b0;
     };
     auto row_a = [&](const Unit &w) { return w.m0 + (int)rank * kRows; };
@@ -234,12 +284,12 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     // The first slabs of the operand that is not a token's (weights, or X in the weights'
     // gradients) go to L2 before the kernels ahead on the stream have finished: what one of them
     // still writes is written in L2, so what is read behind grid_wait() is right either way.
-    if (warp == kTmaWarp && lane == 0) {
-        const Unit w = unit_of(ustart, shape, ncol);
-        for (int i = 0; i < min(w.ns, ST); ++i) {
-            const int r = row_b(w), k = place(w, i);
-            tma_prefetch_2d(map_b(w, i), BMN ? r : k, BMN ? k : r);
-            if (BMN && half > 64) tma_prefetch_2d(map_b(w, i), r + 64, k);
+    Unit w, w0;
+    if (warp == kTmaWarp && unit_at<FORM>(0, shape, ncol, &w0) && lane == 0) {
+        for (int i = 0; i < min(w0.ns, ST); ++i) {
+            const int r = row_b(w0), k = place(w0, i);
+            tma_prefetch_2d(map_b(w0, i), BMN ? r : k, BMN ? k : r);
+            if (BMN && half > 64) tma_prefetch_2d(map_b(w0, i), r + 64, k);
         }
     }
     __syncwarp();
@@ -253,30 +303,40 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         int it = 0, s = 0;
         uint32_t phase = 1;
         bool stop = false;
-        for (int u = ustart; u < shape.units && !stop; u += ustep) {
-            const Unit w = unit_of(u, shape, ncol);
+        for (int j = 0; !stop && unit_at<FORM>(j, shape, ncol, &w); ++j) {
             const int ra = row_a(w), rb = row_b(w);
-            for (int i = 0; i < w.ns; ++i, ++it) {
-                const CUtensorMap *ma = map_a(w, i), *mb = map_b(w, i);
-                const int k = place(w, i);
-                const uint32_t sa = smem_u32(base) + s * ring::stage, sb = sa + ring::a_bytes;
-                const uint32_t fb = lead + 8 * s;
-                if (!warp_wait(empty_bar(s), phase, abort_flag, err)) {
-                    stop = true;
-                    break;
-                }
-                if (lane == 0) {
-                    // both CTAs' copies complete on the first CTA's barrier, which expects both
-                    if (rank == 0) mbar_expect_tx(full_bar(s), 2 * tx);
-                    tma_load_2d_pair(sa, ma, fb, AMN ? ra : k, AMN ? k : ra);
-                    if (AMN) tma_load_2d_pair(sa + 8192, ma, fb, ra + 64, k);
-                    tma_load_2d_pair(sb, mb, fb, BMN ? rb : k, BMN ? k : rb);
-                    if (BMN && half > 64) tma_load_2d_pair(sb + 8192, mb, fb, rb + 64, k);
-                }
-                __syncwarp();
-                if (++s == ST) {
-                    s = 0;
-                    phase ^= 1;
+            const bool amn = a_mn(j);
+            // dX: the slabs of its first product, then those of the second
+            constexpr bool two = FORM == kDx || FORM == kBoth;
+            const int cut = two && !amn ? max(0, min(w.ns, shape.seg_slabs - w.s0)) : w.ns;
+            for (int seg = 0; seg < (two ? 2 : 1) && !stop; ++seg) {
+                const int i0 = seg ? cut : 0, i1 = seg ? w.ns : cut;
+                const CUtensorMap *ma = map_a(w, i0), *mb = map_b(w, i0);
+                int k = place(w, i0);
+                for (int i = i0; i < i1; ++i, ++it, k += kElems) {
+                    const uint32_t sa = smem_u32(base) + s * ring::stage, sb = sa + ring::a_bytes;
+                    const uint32_t fb = lead + 8 * s;
+                    if (!warp_wait(empty_bar(s), phase, abort_flag, err)) {
+                        stop = true;
+                        break;
+                    }
+                    if (lane == 0) {
+                        // both CTAs' copies complete on the first CTA's barrier, which expects both
+                        if (rank == 0) mbar_expect_tx(full_bar(s), 2 * tx);
+                        if (amn) {
+                            tma_load_2d_pair(sa, ma, fb, ra, k);
+                            tma_load_2d_pair(sa + 8192, ma, fb, ra + 64, k);
+                        } else {
+                            tma_load_2d_pair(sa, ma, fb, k, ra);
+                        }
+                        tma_load_2d_pair(sb, mb, fb, BMN ? rb : k, BMN ? k : rb);
+                        if (BMN && half > 64) tma_load_2d_pair(sb + 8192, mb, fb, rb + 64, k);
+                    }
+                    __syncwarp();
+                    if (++s == ST) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }
@@ -295,31 +355,35 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         }
     } else if (warp == kMmaWarp && rank == 0) {
         // ---------------- MMA issue for both CTAs ----------------
-        const uint32_t idesc = ffn_instr_desc<I8, T, AMN, BMN>(kTileM, bn);
-        int s = 0, j = 0;
+        int s = 0;
         uint32_t phase = 0;
         bool stop = false;
-        for (int u = ustart; u < shape.units && !stop; u += ustep, ++j) {
-            const Unit w = unit_of(u, shape, ncol);
+        for (int j = 0; !stop && unit_at<FORM>(j, shape, ncol, &w); ++j) {
             const int b = j & 1;
             if (!warp_wait(acce_bar(b), ((j >> 1) & 1) ^ 1, abort_flag, err)) break;
             tc_fence_after();
             const uint32_t dtm = tmem_base + (uint32_t)(b * kMaxBn);
+            const bool amn = a_mn(j);
+            const uint32_t idesc = amn ? ffn_instr_desc<I8, T, true, BMN>(kTileM, bn)
+                                       : ffn_instr_desc<I8, T, false, BMN>(kTileM, bn);
+            // 32 bytes of a K-major slab, or 16 rows (2048 B) of an MN-major one, per MMA
+            const uint32_t ka = amn ? 128 : 2;
+            constexpr uint32_t kb = BMN ? 128 : 2;
             for (int i = 0; i < w.ns; ++i) {
                 const uint32_t sa = smem_u32(base) + s * ring::stage, sb = sa + ring::a_bytes;
-                const uint64_t da = AMN ? sw128_desc_mn(sa, 8192) : sw128_desc(sa);
+                const uint64_t da = amn ? sw128_desc_mn(sa, 8192) : sw128_desc(sa);
                 const uint64_t db = BMN ? sw128_desc_mn(sb, 8192) : sw128_desc(sb);
+                const uint64_t da1 = da + ka, da2 = da1 + ka, da3 = da2 + ka;
                 if (!warp_wait(full_bar(s), phase, abort_flag, err)) {
                     stop = true;
                     break;
                 }
                 tc_fence_after();
-                // 32 bytes of a K-major slab, or 16 rows (2048 B) of an MN-major one, per MMA
-                constexpr int ka = AMN ? 128 : 2, kb = BMN ? 128 : 2;
                 if (lane == 0) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ffn_mma_pair<I8>(dtm, da + ka * k, db + kb * k, idesc, (i | k) != 0 ? 1u : 0u);
+                    ffn_mma_pair<I8>(dtm, da, db, idesc, i != 0 ? 1u : 0u);
+                    ffn_mma_pair<I8>(dtm, da1, db + kb, idesc, 1u);
+                    ffn_mma_pair<I8>(dtm, da2, db + 2 * kb, idesc, 1u);
+                    ffn_mma_pair<I8>(dtm, da3, db + 3 * kb, idesc, 1u);
                     mma_commit_pair_both(empty_bar(s));
                 }
                 __syncwarp();
@@ -357,23 +421,26 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         auto first_row = [&](const Unit &w) { return w.m0 + (int)rank * kRows + quarter * 32; };
         auto row_scale = [&](const Unit &w) {
             const int m = first_row(w) + lane;
-            return m < shape.M ? out.sa[m] : 0.f;
+            return m < shape.x.M ? out.sa[m] : 0.f;
         };
-        Unit next = unit_of(ustart, shape, ncol);
+        Unit next;
+        bool more = unit_at<FORM>(0, shape, ncol, &next);
         float sa_next = 0.f;
         if constexpr (I8) {
             sa_next = row_scale(next);
             factors(next, first);
         }
-        int j = 0;
-        for (int u = ustart; u < shape.units; u += ustep, ++j) {
-            const Unit w = next;
+        for (int j = 0; more; ++j) {
+            w = next;
+            const bool weights = a_mn(j);
+            const int M = weights ? shape.w.M : shape.x.M;
+            const int parts = weights ? shape.w.parts : shape.x.parts;
             const int b = j & 1;
             const int m = first_row(w);                               // the warp's first row
-            const int rows = min(32, shape.M - m);
+            const int rows = min(32, M - m);
             const int nc = min(ncol, N - w.n0);
             sa = sa_next;
-            if (u + ustep < shape.units) next = unit_of(u + ustep, shape, ncol);
+            more = unit_at<FORM>(j + 1, shape, ncol, &next);
             if constexpr (I8) sa_next = row_scale(next);
             bool ok = mbar_wait(accf_bar(b), (j >> 1) & 1, abort_flag, err);
             tc_fence_after();
@@ -458,9 +525,10 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                                 write(uw, out.c2);
                             }
                         }
-                    } else if (FORM != kScaled && shape.parts > 1) {
-                        const size_t row = (size_t)(w.which * shape.parts + w.part) * shape.M + m;
-                        float *dst = out.part + row * N + w.n0 + c;
+                    } else if (is_grad(FORM) && parts > 1) {
+                        const int part = w.which == 2 ? parts + w.part : w.part;
+                        float *dst = (weights ? out.part_w : out.part_x) +
+                                     ((size_t)part * M + m) * N + w.n0 + c;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -472,7 +540,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 #pragma unroll
                         for (int q = 0; q < 16; ++q)
                             hw[q] = pack2<T>(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
-                        write(hw, FORM == kDw && w.which ? out.c1 : out.c0);
+                        write(hw, is_grad(FORM) && w.which
+                                      ? (w.which == 1 ? out.c1 : out.c2)
+                                      : out.c0);
                     }
                     if constexpr (I8) __syncwarp();       // the column factors are read
                 }
@@ -500,11 +570,20 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 
 // ---- host side -------------------------------------------------------------------------------------
 
+// Tiles of w that a pair takes in place of its missing last tile of x
+int extra_tiles(const Work &x, const Work &w, int pairs)
+{
+    const int rem = x.units % pairs;
+    if (rem == 0 || w.units == 0) return 0;
+    const int fit = (x.part_slabs + w.part_slabs / 2) / w.part_slabs;
+    return std::min(fit, w.units / (pairs - rem));
+}
+
 template <int FORM, bool I8, typename T>
 cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, const Matrix &b1,
-                        const Shape &shape, const Out &out, unsigned int *err, cudaStream_t stream)
+                        const Matrix &b2, Shape shape, const Out &out, unsigned int *err,
+                        cudaStream_t stream)
 {
-    constexpr bool AMN = FORM == kDw, BMN = FORM == kDx || FORM == kDw;
     auto kern = tile_kernel<FORM, I8, T>;
     // per device: the shared-memory opt-in and the number of pairs that fit at once
     static std::mutex mu;
@@ -536,64 +615,144 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
         }
         pairs = pairs_of[dev];
     }
-    if (shape.units <= 0) return cudaErrorInvalidValue;        // more tiles than an int counts
-    CUtensorMap ta0, ta1, tb0, tb1;
-    // MN-major operands arrive in boxes of 64 rows of the reduction
-    const int a_rows = AMN ? 64 : kRows, b_rows = BMN ? 64 : shape.bn / 2;
-    if (!map_of<I8, T>(&ta0, a0, a_rows) || !map_of<I8, T>(&tb0, b0, b_rows))
+    if (shape.x.units < 0 || shape.w.units < 0) return cudaErrorInvalidValue;    // beyond an int
+    const long long units = (long long)shape.x.units + shape.w.units;
+    pairs = (int)std::min<long long>(units, pairs);
+    shape.full = shape.x.units / pairs;
+    shape.rem = shape.x.units % pairs;
+    shape.extra = extra_tiles(shape.x, shape.w, pairs);
+    CUtensorMap ta0, ta1, ta2, ta3, tb0, tb1, tb2;
+    // MN-major operands arrive in boxes of 64 rows
+    const int b_rows = is_grad(FORM) ? 64 : shape.bn / 2;
+    if (!map_of<I8, T>(&ta0, a0, kRows) || !map_of<I8, T>(&tb0, b0, b_rows))
         return cudaErrorInvalidValue;
-    ta1 = ta0;
-    tb1 = tb0;
-    if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, a_rows)) return cudaErrorInvalidValue;
+    ta1 = ta2 = ta3 = ta0;
+    tb1 = tb2 = tb0;
+    if (a1.p != a0.p && !map_of<I8, T>(&ta1, a1, kRows)) return cudaErrorInvalidValue;
     if (b1.p != b0.p && !map_of<I8, T>(&tb1, b1, b_rows)) return cudaErrorInvalidValue;
-    return launch_dependent(kern, dim3(2 * std::min(shape.units, pairs)), dim3(kThreads),
-                            ring::total, 2, stream, ta0, ta1, tb0, tb1, shape, out, err);
+    if (is_grad(FORM) && (!map_of<I8, T>(&ta2, a0, 64) || !map_of<I8, T>(&ta3, a1, 64) ||
+                          !map_of<I8, T>(&tb2, b2, b_rows)))
+        return cudaErrorInvalidValue;
+    return launch_dependent(kern, dim3(2 * pairs), dim3(kThreads), ring::total, 2, stream, ta0, ta1,
+                            tb0, tb1, ta2, ta3, tb2, shape, out, err);
 }
 
-// Widths that the MMA of a pair takes: multiples of 32 for int8 and of 16 for 16-bit types; for
-// MN-major operands whole chunks of 64 values in each CTA.
-constexpr int kStepI8 = 32, kStep16 = 16, kStepMn = 128;
+// Widths that the MMA of a pair takes: multiples of 32 for int8 and of 16 for 16-bit types. The
+// gradients' MN-major operands come in whole chunks of 64 values a CTA: 128 or 256 columns.
+constexpr int kStepI8 = 32, kStep16 = 16;
 constexpr int kPairs = 74;             // of a B200
 constexpr int kMaxParts = 16;
 
+Work work_of(int M, int N, int ncol, int results, int slabs, int parts)
+{
+    Work k = {};
+    k.M = M;
+    k.tiles_m = ceil_div(M, kTileM);
+    k.slabs = slabs;
+    k.part_slabs = ceil_div(slabs, parts);
+    k.parts = ceil_div(slabs, k.part_slabs);        // no empty part
+    const long long units = (long long)results * k.tiles_m * ceil_div(N, ncol) * k.parts;
+    k.units = units > 0x7fffffffLL ? -1 : (int)units;
+    return k;
+}
+
+// A slab takes 0.34 us in a wave that fills the device, nearly whatever the width: 128 columns
+// 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and L2 delivers
+// little more than 90 GB/s to an SM).
+double slab_us(int bn) { return 0.34 * (0.88 + 0.12 * bn / kMaxBn); }
+
 struct Plan {
-    int bn, parts;
+    int bn;
     double us;                         // estimate for a B200
 };
 
-// Tile width and parts of the reduction with the shortest schedule: whole waves of units over the
-// CTA pairs. A slab takes 0.34 us in a wave that fills the device, nearly whatever the width: 128
-// columns 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and L2
-// delivers little more than 90 GB/s to an SM); so fewest waves win, and among them the narrower
-// tile, whose epilogue is shorter. 2 x 43 tiles of 256 columns on 74 pairs, say, leave most of a
-// second wave idle: 2 x 69 tiles of 160 take the same two waves 15 % faster (509 x 11007 x 4080:
-// 38.3 -> 32.4 us). Parts cost their fp32 sums' way to memory and back and a second kernel.
-Plan plan_tiles(int M, int N, int results, bool gated, int step, int slabs, int max_parts)
+// Tile width of the scaled and gated products: whole waves of tiles over the CTA pairs. Fewest
+// waves win, and among them the narrower tile, whose epilogue is shorter: 2 x 43 tiles of 256
+// columns on 74 pairs, say, leave most of a second wave idle; 2 x 69 tiles of 160 take the same two
+// waves 15 % faster (509 x 11007 x 4080: 38.3 -> 32.4 us).
+Plan plan_tiles(int M, int N, bool gated, int step, int slabs)
 {
-    const long tm = ceil_div(M, kTileM);
-    Plan best{kMaxBn, 1, 1e30};
-    for (int parts = 1; parts <= max_parts; ++parts) {
-        const int part_slabs = ceil_div(slabs, parts);
-        if (parts > 1 && (part_slabs < 8 || ceil_div(slabs, part_slabs) != parts)) continue;
-        for (int bn = kMaxBn; bn >= 64; bn -= step) {
-            const long units = tm * ceil_div(N, gated ? bn / 2 : bn) * results * parts;
-            if (parts > 1 && units > kPairs) continue;
-            const double slab = 0.34 * (0.88 + 0.12 * bn / kMaxBn);
-            double us = 3.5 + (double)((units + kPairs - 1) / kPairs) * part_slabs * slab;
-            if (parts > 1) us += 2.5 + (double)results * M * N * 8 * parts / 5e6;
-            if (us < best.us - 1e-9) best = Plan{bn, parts, us};
+    const long long tm = ceil_div(M, kTileM);
+    Plan best{kMaxBn, 1e30};
+    for (int bn = kMaxBn; bn >= 64; bn -= step) {
+        const long long units = tm * ceil_div(N, gated ? bn / 2 : bn);
+        const double us = 3.5 + (double)((units + kPairs - 1) / kPairs) * slabs * slab_us(bn);
+        if (us < best.us - 1e-9) best = Plan{bn, us};
+    }
+    return best;
+}
+
+// Tile width and parts of the gradients of one launch. Parts cost their fp32 sums' way to memory and
+// back and a second kernel; they are tried while the pairs have at most two tiles each.
+struct GradTiles {
+    int bn, parts_x, parts_w;
+    double us;
+};
+
+GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
+{
+    const int slabs_x = 2 * ceil_div(F, 64), slabs_w = ceil_div(M, 64);
+    const int most = dx && dw ? 2 * kPairs : kPairs * 3 / 2;     // units: 256 KB of sums each
+    GradTiles best{kMaxBn, 1, 1, 1e30};
+    for (int bn = kMaxBn; bn >= kMaxBn / 2; bn /= 2) {
+        const Work x1 = work_of(M, K, bn, 1, slabs_x, 1), w1 = work_of(F, K, bn, 2, slabs_w, 1);
+        if (x1.units < 0 || w1.units < 0) continue;
+        auto consider = [&](int px, int pw) {
+            // parts keep eight slabs
+            if ((px > 1 && slabs_x < 8 * px) || (pw > 1 && slabs_w < 8 * pw)) return;
+            const long long units =
+                (dx ? (long long)x1.units * px : 0) + (dw ? (long long)w1.units * pw : 0);
+            if ((px > 1 || pw > 1) && units > most) return;
+            const Work x = dx ? (px > 1 ? work_of(M, K, bn, 1, slabs_x, px) : x1) : Work{};
+            const Work w = dw ? (pw > 1 ? work_of(F, K, bn, 2, slabs_w, pw) : w1) : Work{};
+            const int pairs = (int)std::min<long long>((long long)x.units + w.units, kPairs);
+            const int full = x.units / pairs, rem = x.units % pairs;
+            const int extra = extra_tiles(x, w, pairs);
+            long long slabs = (long long)full * x.part_slabs;
+            if (rem > 0) slabs += std::max(x.part_slabs, extra * w.part_slabs);
+            const int left = w.units - (rem > 0 ? extra * (pairs - rem) : 0);
+            slabs += (long long)ceil_div(left, pairs) * w.part_slabs;
+            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.08 : 1.0);
+            if (x.parts > 1) us += 2.5 + (double)M * K * 8 * x.parts / 5e6;
+            if (w.parts > 1) us += 2.5 + (double)2 * F * K * 8 * w.parts / 5e6;
+            if (us < best.us - 1e-9)
+                best = GradTiles{bn, std::max(1, x.parts), std::max(1, w.parts), us};
+        };
+        consider(1, 1);
+        const long long least =
+            std::min(dx ? x1.units : 0x7fffffff, dw ? w1.units : 0x7fffffff);
+        for (int parts = 2; parts <= kMaxParts && least * parts <= most; ++parts) {
+            if (dx) consider(parts, 1);
+            if (dw) consider(1, parts);
+            if (dx && dw) consider(parts, parts);
         }
     }
     return best;
 }
 
-Plan plan_dx(int M, int F, int K)
+// How the gradients are computed: by the sizes alone, not by what is asked for, so that dX or the
+// weights' gradients by themselves are those of the whole call, bit for bit.
+struct GradPlan {
+    bool together;                     // one launch (kBoth) for dX and the weights' gradients
+    GradTiles x, w;
+    double us;
+};
+
+GradPlan plan_grad(int M, int F, int K, bool with_dx)
 {
-    return plan_tiles(M, K, 1, false, kStepMn, 2 * ceil_div(F, 64), kMaxParts);
-}
-Plan plan_dw(int M, int F, int K)
-{
-    return plan_tiles(F, K, 2, false, kStepMn, ceil_div(M, 64), kMaxParts);
+    GradPlan p = {};
+    p.w = grad_tiles(M, F, K, false, true);
+    p.us = p.w.us;
+    if (!with_dx) return p;
+    p.x = grad_tiles(M, F, K, true, false);
+    p.us += p.x.us;
+    const GradTiles both = grad_tiles(M, F, K, true, true);
+    if (both.us < p.us) {
+        p.together = true;
+        p.x = p.w = both;
+        p.us = both.us;
+    }
+    return p;
 }
 
 // Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
@@ -619,30 +778,23 @@ join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n
 }
 
 template <typename T>
-cudaError_t join_parts(const float *part, void *c0, void *c1, const Shape &s,
+cudaError_t join_parts(const float *part, void *c0, void *c1, const Work &k, int N,
                        cudaStream_t stream)
 {
-    const long long n = (long long)s.M * s.N;
+    const long long n = (long long)k.M * N;
     const dim3 grid((unsigned)((n / 8 + 255) / 256), c1 ? 2 : 1);
     return launch_dependent(join_kernel<T>, grid, dim3(256), 0, 1, stream, part,
-                            static_cast<T *>(c0), static_cast<T *>(c1), s.parts, n);
+                            static_cast<T *>(c0), static_cast<T *>(c1), k.parts, n);
 }
 
-Shape shape_of(int M, int N, int bn, int ncol, int results, int seg_slabs, int segs, int parts, int act)
+Shape shape_of(int M, int N, int bn, int ncol, int slabs, int act)
 {
-    Shape s;
-    s.M = M;
+    Shape s = {};
     s.N = N;
-    s.bn = bn;
-    s.tiles_m = ceil_div(M, kTileM);
     s.tiles_n = ceil_div(N, ncol);
-    s.seg_slabs = seg_slabs;
-    s.slabs = segs * seg_slabs;
-    s.part_slabs = ceil_div(s.slabs, parts);
-    s.parts = ceil_div(s.slabs, s.part_slabs);      // no empty part
-    const long long units = (long long)results * s.tiles_m * s.tiles_n * s.parts;
-    s.units = units > 0x7fffffffLL ? 0 : (int)units;
+    s.bn = bn;
     s.act = act;
+    s.x = work_of(M, N, ncol, 1, slabs, 1);
     return s;
 }
 
@@ -650,17 +802,17 @@ Shape shape_of(int M, int N, int bn, int ncol, int results, int seg_slabs, int s
 
 double tile_us(int M, int N, bool gated, bool i8, int slabs)
 {
-    return plan_tiles(M, N, 1, gated, i8 ? kStepI8 : kStep16, slabs, 1).us;
+    return plan_tiles(M, N, gated, i8 ? kStepI8 : kStep16, slabs).us;
 }
 
-double tile_dx_us(int M, int F, int K) { return plan_dx(M, F, K).us; }
+double tile_grad_us(int M, int F, int K, bool with_dx) { return plan_grad(M, F, K, with_dx).us; }
 
-size_t tile_grad_part_bytes(int M, int F, int K)
+size_t tile_grad_part_bytes(int M, int F, int K, bool with_dx)
 {
-    const Plan x = plan_dx(M, F, K), w = plan_dw(M, F, K);
-    const size_t nx = x.parts > 1 ? (size_t)x.parts * M * K : 0;
-    const size_t nw = w.parts > 1 ? (size_t)w.parts * 2 * F * K : 0;
-    return std::max(nx, nw) * 4;
+    const GradPlan p = plan_grad(M, F, K, with_dx);
+    size_t n = p.w.parts_w > 1 ? (size_t)p.w.parts_w * 2 * F * K : 0;
+    if (with_dx && p.x.parts_x > 1) n += (size_t)p.x.parts_x * M * K;
+    return n * 4;
 }
 
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
@@ -669,13 +821,13 @@ cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaSt
     const bool gated = p.W1 != nullptr;
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
     const Matrix w1{gated ? p.W1 : p.W, (uint64_t)p.N, K, K};
-    const Out out{p.C, nullptr, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
+    const Out out{p.C, nullptr, nullptr, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
     const int slabs = ceil_div(p.K, 128);
-    const int bn = plan_tiles(p.M, p.N, 1, gated, kStepI8, slabs, 1).bn;
-    const Shape shape = shape_of(p.M, p.N, bn, gated ? bn / 2 : bn, 1, slabs, 1, 1, p.act);
+    const int bn = plan_tiles(p.M, p.N, gated, kStepI8, slabs).bn;
+    const Shape shape = shape_of(p.M, p.N, bn, gated ? bn / 2 : bn, slabs, p.act);
     QG_DISPATCH_16(p.dtype, T, {
-        if (gated) return launch_tile<kGated, true, T>(a, a, w, w1, shape, out, err, stream);
-        return launch_tile<kScaled, true, T>(a, a, w, w1, shape, out, err, stream);
+        if (gated) return launch_tile<kGated, true, T>(a, a, w, w1, w, shape, out, err, stream);
+        return launch_tile<kScaled, true, T>(a, a, w, w1, w, shape, out, err, stream);
     });
 }
 
@@ -684,42 +836,61 @@ cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStre
     const uint64_t K = p.K, pitch = K * 2;
     const Matrix x{p.X, (uint64_t)p.M, K, pitch};
     const Matrix g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
-    const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr, nullptr};
+    Out out = {};
+    out.c0 = p.H;
+    out.c1 = p.G;
+    out.c2 = p.U;
     const int slabs = ceil_div(p.K, 64);
-    const int bn = plan_tiles(p.M, p.F, 1, true, kStep16, slabs, 1).bn;
-    const Shape shape = shape_of(p.M, p.F, bn, bn / 2, 1, slabs, 1, 1, p.act);
+    const int bn = plan_tiles(p.M, p.F, true, kStep16, slabs).bn;
+    const Shape shape = shape_of(p.M, p.F, bn, bn / 2, slabs, p.act);
     QG_DISPATCH_16(p.dtype, T, {
-        return launch_tile<kGated, false, T>(x, x, g, u, shape, out, err, stream);
+        return launch_tile<kGated, false, T>(x, x, g, u, g, shape, out, err, stream);
     });
 }
 
-cudaError_t launch_tile_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
+cudaError_t launch_tile_grad(const GatedGrad &p, bool with_dx, unsigned int *err,
+                             cudaStream_t stream)
 {
+    const bool dx = with_dx && p.dX, dw = p.dWg != nullptr;
+    if (!dx && !dw) return cudaSuccess;
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
-    const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2};
-    const Out out{p.dX, nullptr, nullptr, p.part, nullptr, nullptr, nullptr, nullptr};
-    const Plan plan = plan_dx(p.M, p.F, p.K);
-    const Shape shape = shape_of(p.M, p.K, plan.bn, plan.bn, 1, ceil_div(p.F, 64), 2, plan.parts, 0);
+    const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2}, x{p.X, M, K, K * 2};
+    const GradPlan plan = plan_grad(p.M, p.F, p.K, with_dx);
+    auto grad_shape = [&](const GradTiles &t, bool of_x, bool of_w) {
+        Shape s = {};
+        s.N = p.K;
+        s.bn = t.bn;
+        s.tiles_n = ceil_div(p.K, t.bn);
+        s.seg_slabs = ceil_div(p.F, 64);
+        if (of_x) s.x = work_of(p.M, p.K, t.bn, 1, 2 * s.seg_slabs, t.parts_x);
+        if (of_w) s.w = work_of(p.F, p.K, t.bn, 2, ceil_div(p.M, 64), t.parts_w);
+        return s;
+    };
+    const bool both = plan.together && dx && dw;
+    const Shape sx = dx ? grad_shape(plan.x, true, both) : Shape{};
+    const Shape sw = grad_shape(plan.w, false, dw);
+    Out out = {};
+    out.c0 = p.dX;
+    out.c1 = p.dWg;
+    out.c2 = p.dWu;
+    out.part_x = p.part;
+    out.part_w = p.part;
+    if (with_dx && plan.x.parts_x > 1) out.part_w += (size_t)plan.x.parts_x * p.M * p.K;
     QG_DISPATCH_16(p.dtype, T, {
-        const cudaError_t e = launch_tile<kDx, false, T>(dg, du, wg, wu, shape, out, err, stream);
-        if (e != cudaSuccess || shape.parts == 1) return e;
-        return join_parts<T>(p.part, p.dX, nullptr, shape, stream);
-    });
-}
-
-cudaError_t launch_tile_dw(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
-{
-    const uint64_t M = p.M, F = p.F, K = p.K;
-    const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
-    const Matrix x{p.X, M, K, K * 2};
-    const Out out{p.dWg, p.dWu, nullptr, p.part, nullptr, nullptr, nullptr, nullptr};
-    const Plan plan = plan_dw(p.M, p.F, p.K);
-    const Shape shape = shape_of(p.F, p.K, plan.bn, plan.bn, 2, ceil_div(p.M, 64), 1, plan.parts, 0);
-    QG_DISPATCH_16(p.dtype, T, {
-        const cudaError_t e = launch_tile<kDw, false, T>(dg, du, x, x, shape, out, err, stream);
-        if (e != cudaSuccess || shape.parts == 1) return e;
-        return join_parts<T>(p.part, p.dWg, p.dWu, shape, stream);
+        cudaError_t e = cudaSuccess;
+        if (both) {
+            e = launch_tile<kBoth, false, T>(dg, du, wg, wu, x, sx, out, err, stream);
+        } else {
+            if (dx) e = launch_tile<kDx, false, T>(dg, du, wg, wu, x, sx, out, err, stream);
+            if (e == cudaSuccess && dw)
+                e = launch_tile<kDw, false, T>(dg, du, wg, wu, x, sw, out, err, stream);
+        }
+        if (e == cudaSuccess && dx && sx.x.parts > 1)
+            e = join_parts<T>(out.part_x, p.dX, nullptr, sx.x, p.K, stream);
+        if (e == cudaSuccess && dw && sw.w.parts > 1)
+            e = join_parts<T>(out.part_w, p.dWg, p.dWu, sw.w, p.K, stream);
+        return e;
     });
 }
 
