@@ -26,6 +26,11 @@ int padded_f(int F) { return (F + 7) & ~7; }
 // bytes of dG (and of dU): M rows of padded_f(F) 16-bit values
 size_t grad_bytes(int M, int F) { return round256((size_t)M * padded_f(F) * 2); }
 
+size_t backward_bytes(const GradPlan &plan, int M, int F, int K)
+{
+    return 2 * grad_bytes(M, F) + round256(grad_part_bytes(plan, M, F, K));
+}
+
 } // namespace
 } // namespace qg
 
@@ -105,7 +110,7 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
 size_t qgemm_dense_gated_backward_workspace_bytes(int M, int F, int K)
 {
     if (M <= 0 || F <= 0 || K <= 0 || K % 8) return 0;
-    return 2 * grad_bytes(M, F) + round256(gated_backward_part_bytes(M, F, K));
+    return backward_bytes(plan_gated_backward(M, F, K), M, F, K);
 }
 
 qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
@@ -121,15 +126,15 @@ qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *
         !aligned(G, 16) || !aligned(U, 16) || !aligned(dX, 16) || !aligned(dWg, 16) ||
         !aligned(dWu, 16) || !aligned(workspace, 256))
         return QG_ERR_ALIGNMENT;
-    if (workspace_bytes < qgemm_dense_gated_backward_workspace_bytes(M, F, K))
-        return QG_ERR_SCRATCH_TOO_SMALL;
+    const GradPlan plan = plan_gated_backward(M, F, K);
+    if (workspace_bytes < backward_bytes(plan, M, F, K)) return QG_ERR_SCRATCH_TOO_SMALL;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);
     if (s != QG_OK) return s;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const GatedGrad p{dH, X, Wg, Wu, G, U, dX, dWg, dWu, ws, ws + grad_bytes(M, F), M, F, K, act,
-                      dtype, padded_f(F), reinterpret_cast<float *>(ws + 2 * grad_bytes(M, F))};
+                      dtype, padded_f(F), reinterpret_cast<float *>(ws + 2 * grad_bytes(M, F)), plan};
     return launched(launch_gated_backward(p, err, stream));
 }
 

@@ -8,7 +8,9 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewTokens = 64;         // up to here the weights' stream is the bound in every case
+// Up to here the few-token kernel without asking the estimates: the weights' stream is the bound (at
+// 100 tokens, 512 to 11008 columns by 2048 to 11008: 6 to 36 us against 9 to 48 us of the tiles).
+constexpr int kFewTokens = 64;
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
@@ -90,7 +92,8 @@ template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cuda
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)ctas), block(kThreads);
     if (p.F % 8 == 0)
-        return launch_dependent(grad_act_kernel<T, ACT>, grid, block, 0, 1, stream, dH, G, U, dG, dU, n);
+        return launch_dependent(grad_act_kernel<T, ACT>, grid, block, 0, 1, stream, dH, G, U, dG,
+                                dU, n);
     if (p.F % 2 == 0)
         return launch_dependent(grad_act_rows_kernel<T, ACT, true>, grid, block, 0, 1, stream, dH, G,
                                 U, dG, dU, p.F, p.Fp);
@@ -98,19 +101,28 @@ template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cuda
                             dG, dU, p.F, p.Fp);
 }
 
-// Whether dX goes to the few-token kernel, and only the weights' gradients to the tiles, or all of
-// them to one launch of tiles. By the sizes alone, not by what is asked for.
-bool dx_by_few(int M, int F, int K)
-{
-    return M <= kFewTokens ||
-           small_dx_us(M, F, K) + tile_grad_us(M, F, K, false) < tile_grad_us(M, F, K, true);
-}
-
 } // namespace
 
-size_t gated_backward_part_bytes(int M, int F, int K)
+GradPlan plan_gated_backward(int M, int F, int K)
 {
-    return tile_grad_part_bytes(M, F, K, !dx_by_few(M, F, K));
+    GradPlan p = {};
+    p.w = grad_tiles(M, F, K, false, true);
+    p.few = M <= kFewTokens;
+    if (p.few) return p;
+    p.x = grad_tiles(M, F, K, true, false);
+    const GradTiles both = grad_tiles(M, F, K, true, true);
+    p.together = both.us < p.x.us + p.w.us;
+    p.few = small_dx_us(M, F, K) + p.w.us < (p.together ? both.us : p.x.us + p.w.us);
+    if (p.few) p.together = false;
+    else if (p.together) p.x = p.w = both;
+    return p;
+}
+
+size_t grad_part_bytes(const GradPlan &p, int M, int F, int K)
+{
+    size_t n = p.w.parts_w > 1 ? (size_t)p.w.parts_w * 2 * F * K : 0;
+    if (!p.few && p.x.parts_x > 1) n += (size_t)p.x.parts_x * M * K;
+    return n * 4;
 }
 
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
@@ -138,9 +150,8 @@ cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStr
             e = run_grad_act<T, ACT>(p, stream);
         });
     });
-    const bool few = dx_by_few(p.M, p.F, p.K);
-    if (e == cudaSuccess && few && p.dX) e = launch_small_dx(p, err, stream);
-    if (e == cudaSuccess) e = launch_tile_grad(p, !few, err, stream);
+    if (e == cudaSuccess && p.plan.few && p.dX) e = launch_small_dx(p, err, stream);
+    if (e == cudaSuccess) e = launch_tile_grad(p, err, stream);
     return e;
 }
 

@@ -161,12 +161,25 @@ struct GatedProblem {       // 16-bit operands, forward
     void *H, *G, *U;
     int M, F, K, act, dtype;
 };
+// Tile width and parts of the reductions of a launch of gradient tiles; us: estimate for a B200
+struct GradTiles {
+    int bn, parts_x, parts_w;
+    double us;
+};
+// How the gradients are computed: by the sizes alone, not by what is asked for, so that dX or the
+// weights' gradients by themselves are those of the whole call, bit for bit.
+struct GradPlan {
+    bool few;               // dX by the few-token kernel, only the weights' gradients by tiles
+    bool together;          // tiles of dX and of the weights' gradients in one launch
+    GradTiles x, w;
+};
 struct GatedGrad {          // backward; dG, dU and part live in the caller's workspace
     const void *dH, *X, *Wg, *Wu, *G, *U;
     void *dX, *dWg, *dWu, *dG, *dU;
     int M, F, K, act, dtype;
     int Fp;                 // row pitch of dG and dU in elements (a multiple of 8)
-    float *part;            // partial sums, gated_backward_part_bytes() bytes
+    float *part;            // partial sums, grad_part_bytes() bytes
+    GradPlan plan;
 };
 
 cudaError_t launch_quant_int8_tokens(const void *X, int8_t *Q, float *scales, int M, int K,
@@ -174,18 +187,16 @@ cudaError_t launch_quant_int8_tokens(const void *X, int8_t *Q, float *scales, in
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_dense_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
-// bytes of GatedGrad::part
-size_t gated_backward_part_bytes(int M, int F, int K);
+GradPlan plan_gated_backward(int M, int F, int K);
+size_t grad_part_bytes(const GradPlan &plan, int M, int F, int K);
 
 // Large tiles (ffn_tile.cu) and few tokens (ffn_small.cu): each takes any sizes. The estimates, in
 // microseconds, choose between them; slabs: 128-byte steps of the reduction.
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
-cudaError_t launch_tile_grad(const GatedGrad &p, bool with_dx, unsigned int *err,
-                             cudaStream_t stream);
+cudaError_t launch_tile_grad(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
 double tile_us(int M, int N, bool gated, bool i8, int slabs);
-double tile_grad_us(int M, int F, int K, bool with_dx);
-size_t tile_grad_part_bytes(int M, int F, int K, bool with_dx);
+GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw);
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream);

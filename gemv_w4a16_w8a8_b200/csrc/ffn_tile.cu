@@ -682,79 +682,6 @@ Plan plan_tiles(int M, int N, bool gated, int step, int slabs)
     return best;
 }
 
-// Tile width and parts of the gradients of one launch. Parts cost their fp32 sums' way to memory and
-// back and a second kernel; they are tried while the pairs have at most two tiles each.
-struct GradTiles {
-    int bn, parts_x, parts_w;
-    double us;
-};
-
-GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
-{
-    const int slabs_x = 2 * ceil_div(F, 64), slabs_w = ceil_div(M, 64);
-    const int most = dx && dw ? 2 * kPairs : kPairs * 3 / 2;     // units: 256 KB of sums each
-    GradTiles best{kMaxBn, 1, 1, 1e30};
-    for (int bn = kMaxBn; bn >= kMaxBn / 2; bn /= 2) {
-        const Work x1 = work_of(M, K, bn, 1, slabs_x, 1), w1 = work_of(F, K, bn, 2, slabs_w, 1);
-        if (x1.units < 0 || w1.units < 0) continue;
-        auto consider = [&](int px, int pw) {
-            // parts keep eight slabs
-            if ((px > 1 && slabs_x < 8 * px) || (pw > 1 && slabs_w < 8 * pw)) return;
-            const long long units =
-                (dx ? (long long)x1.units * px : 0) + (dw ? (long long)w1.units * pw : 0);
-            if ((px > 1 || pw > 1) && units > most) return;
-            const Work x = dx ? (px > 1 ? work_of(M, K, bn, 1, slabs_x, px) : x1) : Work{};
-            const Work w = dw ? (pw > 1 ? work_of(F, K, bn, 2, slabs_w, pw) : w1) : Work{};
-            const int pairs = (int)std::min<long long>((long long)x.units + w.units, kPairs);
-            const int full = x.units / pairs, rem = x.units % pairs;
-            const int extra = extra_tiles(x, w, pairs);
-            long long slabs = (long long)full * x.part_slabs;
-            if (rem > 0) slabs += std::max(x.part_slabs, extra * w.part_slabs);
-            const int left = w.units - (rem > 0 ? extra * (pairs - rem) : 0);
-            slabs += (long long)ceil_div(left, pairs) * w.part_slabs;
-            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.08 : 1.0);
-            if (x.parts > 1) us += 2.5 + (double)M * K * 8 * x.parts / 5e6;
-            if (w.parts > 1) us += 2.5 + (double)2 * F * K * 8 * w.parts / 5e6;
-            if (us < best.us - 1e-9)
-                best = GradTiles{bn, std::max(1, x.parts), std::max(1, w.parts), us};
-        };
-        consider(1, 1);
-        const long long least =
-            std::min(dx ? x1.units : 0x7fffffff, dw ? w1.units : 0x7fffffff);
-        for (int parts = 2; parts <= kMaxParts && least * parts <= most; ++parts) {
-            if (dx) consider(parts, 1);
-            if (dw) consider(1, parts);
-            if (dx && dw) consider(parts, parts);
-        }
-    }
-    return best;
-}
-
-// How the gradients are computed: by the sizes alone, not by what is asked for, so that dX or the
-// weights' gradients by themselves are those of the whole call, bit for bit.
-struct GradPlan {
-    bool together;                     // one launch (kBoth) for dX and the weights' gradients
-    GradTiles x, w;
-    double us;
-};
-
-GradPlan plan_grad(int M, int F, int K, bool with_dx)
-{
-    GradPlan p = {};
-    p.w = grad_tiles(M, F, K, false, true);
-    p.us = p.w.us;
-    if (!with_dx) return p;
-    p.x = grad_tiles(M, F, K, true, false);
-    p.us += p.x.us;
-    const GradTiles both = grad_tiles(M, F, K, true, true);
-    if (both.us < p.us) {
-        p.together = true;
-        p.x = p.w = both;
-        p.us = both.us;
-    }
-    return p;
-}
-
 // Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -800,19 +727,52 @@ Shape shape_of(int M, int N, int bn, int ncol, int slabs, int act)
 
 } // namespace
 
+// Tile width and parts of the gradients of one launch. Parts cost their fp32 sums' way to memory and
+// back and a second kernel; they are tried while the pairs have at most two tiles each.
+GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
+{
+    const int slabs_x = 2 * ceil_div(F, 64), slabs_w = ceil_div(M, 64);
+    const int most = dx && dw ? 2 * kPairs : kPairs * 3 / 2;     // units: 256 KB of sums each
+    GradTiles best{kMaxBn, 1, 1, 1e30};
+    for (int bn = kMaxBn; bn >= kMaxBn / 2; bn /= 2) {
+        const Work x1 = work_of(M, K, bn, 1, slabs_x, 1), w1 = work_of(F, K, bn, 2, slabs_w, 1);
+        if (x1.units < 0 || w1.units < 0) continue;
+        auto consider = [&](int px, int pw) {
+            // parts keep eight slabs
+            if ((px > 1 && slabs_x < 8 * px) || (pw > 1 && slabs_w < 8 * pw)) return;
+            const long long units =
+                (dx ? (long long)x1.units * px : 0) + (dw ? (long long)w1.units * pw : 0);
+            if ((px > 1 || pw > 1) && units > most) return;
+            const Work x = dx ? (px > 1 ? work_of(M, K, bn, 1, slabs_x, px) : x1) : Work{};
+            const Work w = dw ? (pw > 1 ? work_of(F, K, bn, 2, slabs_w, pw) : w1) : Work{};
+            const int pairs = (int)std::min<long long>((long long)x.units + w.units, kPairs);
+            const int full = x.units / pairs, rem = x.units % pairs;
+            const int extra = extra_tiles(x, w, pairs);
+            long long slabs = (long long)full * x.part_slabs;
+            if (rem > 0) slabs += std::max(x.part_slabs, extra * w.part_slabs);
+            const int left = w.units - (rem > 0 ? extra * (pairs - rem) : 0);
+            slabs += (long long)ceil_div(left, pairs) * w.part_slabs;
+            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.08 : 1.0);
+            if (x.parts > 1) us += 2.5 + (double)M * K * 8 * x.parts / 5e6;
+            if (w.parts > 1) us += 2.5 + (double)2 * F * K * 8 * w.parts / 5e6;
+            if (us < best.us - 1e-9)
+                best = GradTiles{bn, std::max(1, x.parts), std::max(1, w.parts), us};
+        };
+        consider(1, 1);
+        const long long least =
+            std::min(dx ? x1.units : 0x7fffffff, dw ? w1.units : 0x7fffffff);
+        for (int parts = 2; parts <= kMaxParts && least * parts <= most; ++parts) {
+            if (dx) consider(parts, 1);
+            if (dw) consider(1, parts);
+            if (dx && dw) consider(parts, parts);
+        }
+    }
+    return best;
+}
+
 double tile_us(int M, int N, bool gated, bool i8, int slabs)
 {
     return plan_tiles(M, N, gated, i8 ? kStepI8 : kStep16, slabs).us;
-}
-
-double tile_grad_us(int M, int F, int K, bool with_dx) { return plan_grad(M, F, K, with_dx).us; }
-
-size_t tile_grad_part_bytes(int M, int F, int K, bool with_dx)
-{
-    const GradPlan p = plan_grad(M, F, K, with_dx);
-    size_t n = p.w.parts_w > 1 ? (size_t)p.w.parts_w * 2 * F * K : 0;
-    if (with_dx && p.x.parts_x > 1) n += (size_t)p.x.parts_x * M * K;
-    return n * 4;
 }
 
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
@@ -848,15 +808,14 @@ cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStre
     });
 }
 
-cudaError_t launch_tile_grad(const GatedGrad &p, bool with_dx, unsigned int *err,
-                             cudaStream_t stream)
+cudaError_t launch_tile_grad(const GatedGrad &p, unsigned int *err, cudaStream_t stream)
 {
-    const bool dx = with_dx && p.dX, dw = p.dWg != nullptr;
+    const GradPlan &plan = p.plan;
+    const bool dx = !plan.few && p.dX, dw = p.dWg != nullptr;
     if (!dx && !dw) return cudaSuccess;
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2}, x{p.X, M, K, K * 2};
-    const GradPlan plan = plan_grad(p.M, p.F, p.K, with_dx);
     auto grad_shape = [&](const GradTiles &t, bool of_x, bool of_w) {
         Shape s = {};
         s.N = p.K;
@@ -876,7 +835,7 @@ cudaError_t launch_tile_grad(const GatedGrad &p, bool with_dx, unsigned int *err
     out.c2 = p.dWu;
     out.part_x = p.part;
     out.part_w = p.part;
-    if (with_dx && plan.x.parts_x > 1) out.part_w += (size_t)plan.x.parts_x * p.M * p.K;
+    if (!plan.few && plan.x.parts_x > 1) out.part_w += (size_t)plan.x.parts_x * p.M * p.K;
     QG_DISPATCH_16(p.dtype, T, {
         cudaError_t e = cudaSuccess;
         if (both) {
