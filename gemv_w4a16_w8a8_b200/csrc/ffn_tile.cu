@@ -752,7 +752,7 @@ GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
             if (rem > 0) slabs += std::max(x.part_slabs, extra * w.part_slabs);
             const int left = w.units - (rem > 0 ? extra * (pairs - rem) : 0);
             slabs += (long long)ceil_div(left, pairs) * w.part_slabs;
-            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.08 : 1.0);
+            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.10 : 1.0);
             if (x.parts > 1) us += 2.5 + (double)M * K * 8 * x.parts / 5e6;
             if (w.parts > 1) us += 2.5 + (double)2 * F * K * 8 * w.parts / 5e6;
             if (us < best.us - 1e-9)
