@@ -471,10 +471,16 @@ def _operand(t, dtype, shape, name, index):
     raise ValueError(f"{name} must be contiguous")
 
 
+INT_MAX = 2 ** 31 - 1
+
+
 def _matrix(t, dtype, name):
     """_need for a matrix, by the fewest reads where nothing is wrong."""
     try:
         if t.dtype is dtype and t.dim() == 2 and t.is_cuda and t.is_contiguous():
+            rows, cols = t.shape
+            if rows > INT_MAX or cols > INT_MAX:          # the C entry points take int sizes
+                raise ValueError(f"{name} has more than {INT_MAX} rows or columns")
             return t.shape
     except AttributeError:
         pass

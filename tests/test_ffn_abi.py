@@ -129,3 +129,23 @@ def test_binding_refuses_types_and_names():
         qg.qgemm_dense_gated(x, x, x, act="relu")
     with pytest.raises(ValueError, match="act"):
         qg.qgemm_dense_gated_backward(x, x, x, x, x, x, act="swish")
+
+
+@pytest.mark.parametrize("shape", [(2 ** 31, 8), (2 ** 32 + 5, 8), (1, 2 ** 32 + 16)])
+def test_binding_refuses_sizes_beyond_an_int(shape):
+    """Four billion rows would arrive in C as a handful."""
+    class Huge:
+        dtype = torch.float16
+        is_cuda = True
+
+        def __init__(self):
+            self.shape = shape
+
+        def dim(self):
+            return 2
+
+        def is_contiguous(self):
+            return True
+
+    with pytest.raises(ValueError, match="rows or columns"):
+        qg.quant_int8_tokens(Huge())
