@@ -50,8 +50,7 @@ __device__ __forceinline__ uint2 codes8(const uint4 &v, float up, float inv)
 
 template <typename T, int TPR, bool LONG>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
-quant_tokens_kernel(const T *__restrict__ X, int8_t *__restrict__ Q, float *__restrict__ scales, int M,
-                    int K)
+quant_tokens_kernel(const T *X, int8_t *Q, float *scales, int M, int K)
 {
     constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR, kWarps = TPR / 32;
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
@@ -69,12 +68,12 @@ quant_tokens_kernel(const T *__restrict__ X, int8_t *__restrict__ Q, float *__re
     for (int i = 0; i < kVec; ++i) {
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (t + i * TPR < n)
-            v[i] = LONG ? ld_cached_v4(x + t + i * TPR) : ld_stream_v4(x + t + i * TPR);
+            v[i] = LONG ? ld_behind_cached_v4(x + t + i * TPR) : ld_behind_v4(x + t + i * TPR);
     }
 #pragma unroll
     for (int i = 0; i < kVec; ++i) top = max_abs(top, v[i]);
     if constexpr (LONG)
-        for (int j = t + kVec * TPR; j < n; j += TPR) top = max_abs(top, ld_cached_v4(x + j));
+        for (int j = t + kVec * TPR; j < n; j += TPR) top = max_abs(top, ld_behind_cached_v4(x + j));
     top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
     if constexpr (kWarps > 1) {
         __shared__ uint32_t part[kRows][kWarps];
@@ -95,7 +94,7 @@ quant_tokens_kernel(const T *__restrict__ X, int8_t *__restrict__ Q, float *__re
         if (t + i * TPR < n) q[t + i * TPR] = bad ? make_uint2(0u, 0u) : codes8<T>(v[i], up, inv);
     if constexpr (LONG)
         for (int j = t + kVec * TPR; j < n; j += TPR)
-            q[j] = bad ? make_uint2(0u, 0u) : codes8<T>(ld_cached_v4(x + j), up, inv);
+            q[j] = bad ? make_uint2(0u, 0u) : codes8<T>(ld_behind_cached_v4(x + j), up, inv);
 }
 
 template <typename T, int TPR, bool LONG>

@@ -33,14 +33,13 @@ __device__ __forceinline__ void grad_pair(uint32_t dh, uint32_t g, uint32_t u, u
 
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kThreads)
-grad_act_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__restrict__ U,
-                T *__restrict__ dG, T *__restrict__ dU, size_t n)
+grad_act_kernel(const T *dH, const T *G, const T *U, T *dG, T *dU, size_t n)
 {
     grid_release();
     grid_wait();
     const size_t at = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 8;
     if (at >= n) return;
-    const uint4 h = ld_stream_v4(dH + at), g = ld_stream_v4(G + at), u = ld_stream_v4(U + at);
+    const uint4 h = ld_behind_v4(dH + at), g = ld_behind_v4(G + at), u = ld_behind_v4(U + at);
     uint4 dg, du;
     grad_pair<T, ACT>(h.x, g.x, u.x, dg.x, du.x);
     grad_pair<T, ACT>(h.y, g.y, u.y, dg.y, du.y);
@@ -52,8 +51,7 @@ grad_act_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__re
 
 template <typename T, int ACT, bool PAIRS>
 __global__ void __launch_bounds__(kThreads)
-grad_act_rows_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T *__restrict__ U,
-                     T *__restrict__ dG, T *__restrict__ dU, int F, int Fp)
+grad_act_rows_kernel(const T *dH, const T *G, const T *U, T *dG, T *dU, int F, int Fp)
 {
     grid_release();
     grid_wait();
@@ -61,23 +59,52 @@ grad_act_rows_kernel(const T *__restrict__ dH, const T *__restrict__ G, const T 
     const size_t m = blockIdx.x / spans;
     const int f0 = (int)(blockIdx.x % spans) * kSpan, f1 = min(f0 + kSpan, F);
     const size_t in = m * F, to = m * Fp;
-    if constexpr (PAIRS) {
-#pragma unroll 4
-        for (int f = f0 + 2 * threadIdx.x; f < f1; f += 2 * kThreads) {
-            uint32_t dg, du;
-            grad_pair<T, ACT>(ld_stream_u32(dH + in + f), ld_stream_u32(G + in + f),
-                              ld_stream_u32(U + in + f), dg, du);
-            *reinterpret_cast<uint32_t *>(dG + to + f) = dg;
-            *reinterpret_cast<uint32_t *>(dU + to + f) = du;
-        }
-    } else {
-#pragma unroll 4
-        for (int f = f0 + threadIdx.x; f < f1; f += kThreads) {
-            float v, d;
-            act_both<ACT>(to_f32(G[in + f]), v, d);
-            const float dh = to_f32(dH[in + f]);
-            dG[to + f] = from_f32<T>(dh * to_f32(U[in + f]) * d);
-            dU[to + f] = from_f32<T>(dh * v);
+    // kBatch loads of each matrix in flight, then what is made of them: the loads keep their order
+    constexpr int kBatch = 4, kStep = (PAIRS ? 2 : 1) * kThreads;
+#pragma unroll 1
+    for (int f = f0 + (PAIRS ? 2 : 1) * (int)threadIdx.x; f < f1; f += kBatch * kStep) {
+        if constexpr (PAIRS) {
+            uint32_t h[kBatch] = {}, g[kBatch] = {}, u[kBatch] = {};
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = f + i * kStep;
+                if (at < f1) {
+                    h[i] = ld_behind_u32(dH + in + at);
+                    g[i] = ld_behind_u32(G + in + at);
+                    u[i] = ld_behind_u32(U + in + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = f + i * kStep;
+                uint32_t dg, du;
+                grad_pair<T, ACT>(h[i], g[i], u[i], dg, du);
+                if (at < f1) {
+                    *reinterpret_cast<uint32_t *>(dG + to + at) = dg;
+                    *reinterpret_cast<uint32_t *>(dU + to + at) = du;
+                }
+            }
+        } else {
+            float h[kBatch] = {}, g[kBatch] = {}, u[kBatch] = {};
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = f + i * kStep;
+                if (at < f1) {
+                    h[i] = ld_behind_16<T>(dH + in + at);
+                    g[i] = ld_behind_16<T>(G + in + at);
+                    u[i] = ld_behind_16<T>(U + in + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = f + i * kStep;
+                float v, d;
+                act_both<ACT>(g[i], v, d);
+                if (at < f1) {
+                    dG[to + at] = from_f32<T>(h[i] * u[i] * d);
+                    dU[to + at] = from_f32<T>(h[i] * v);
+                }
+            }
         }
     }
 }

@@ -111,16 +111,65 @@ template <int V> struct Const {
     } while (0)
 
 // ------------------------------------------------------------------------------------------
-// Programmatic dependent launch. Each of these kernels lets its successor's CTAs start as soon as
-// its own have all started, and touches global memory only behind grid_wait(), which returns when
-// the kernels before it on the stream have finished and their writes are visible. So a kernel's
-// launch, barrier and tensor-memory set-up run under the end of its predecessor, and stream order
-// is kept: 1 to 3 us less a call, measured on calls of 2 to 60 us that follow one another.
+// Programmatic dependent launch. grid_wait() returns when the kernels before this one on the stream
+// have finished and their writes are visible; grid_release() lets the next kernel's CTAs start once
+// every CTA of this one has called it. The kernels without tensor cores (quantisation, elementwise
+// half of the gradients, joining of parts) release as soon as they start, the tensor-core kernels
+// when the last of their loads is on its way. Results are written, and operands read, only behind
+// grid_wait(); before it the tensor-core kernels do no more than ask for their first weights to be
+// brought into L2, where a predecessor's writes to them land too. So a kernel's launch, barrier and
+// tensor-memory set-up run under the end of its predecessor, and stream order is kept: 1 to 3 us
+// less a call, measured on calls of 2 to 60 us that follow one another.
+//
+// Such a kernel runs while what it will read is still being written. Its loads are therefore the
+// ld_behind_* below: volatile with a memory clobber, so that the compiler leaves them behind
+// grid_wait(), and not .nc, which asks for data that does not change during the kernel's life.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_behind_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// 16 bytes that are read again
+__device__ __forceinline__ uint4 ld_behind_cached_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_behind_u32(const void *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_behind_f32(const float *p)
+{
+    return __uint_as_float(ld_behind_u32(p));
+}
+
+template <typename T> __device__ __forceinline__ float ld_behind_16(const void *p)
+{
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return unpack2<T>(v).x;
 }
 
 // Launch with `cluster` CTAs a cluster (along x) and programmatic dependent launch.

@@ -199,14 +199,14 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     const bool mine = (int)threadIdx.x < ng * step && n < N;
     float f0[4] = {}, f1[4] = {};
     if (I8 && warp < 4) {
-        scale_s[threadIdx.x] = (int)threadIdx.x < tokens ? out.sa[t0 + threadIdx.x] : 0.f;
+        scale_s[threadIdx.x] = (int)threadIdx.x < tokens ? ld_behind_f32(out.sa + t0 + threadIdx.x) : 0.f;
         if (mine) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int c = min(n + e, N - 1);
-                f0[e] = out.sw[c];
-                if constexpr (FORM == kGated) f1[e] = out.sw1[c];
-                else if (out.bias) f1[e] = to_f32(static_cast<const T *>(out.bias)[c]);
+                f0[e] = ld_behind_f32(out.sw + c);
+                if constexpr (FORM == kGated) f1[e] = ld_behind_f32(out.sw1 + c);
+                else if (out.bias) f1[e] = ld_behind_16<T>(static_cast<const T *>(out.bias) + c);
             }
         }
     }

@@ -414,14 +414,14 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         float sa = 0.f, f0 = 0.f, f1 = 0.f;
         auto factors = [&](const Unit &w, int c) {
             const int n = min(w.n0 + min(c + lane, ncol - 1), N - 1);
-            f0 = out.sw[n];
-            if constexpr (FORM == kGated) f1 = out.sw1[n];
-            else f1 = out.bias ? to_f32(static_cast<const T *>(out.bias)[n]) : 0.f;
+            f0 = ld_behind_f32(out.sw + n);
+            if constexpr (FORM == kGated) f1 = ld_behind_f32(out.sw1 + n);
+            else f1 = out.bias ? ld_behind_16<T>(static_cast<const T *>(out.bias) + n) : 0.f;
         };
         auto first_row = [&](const Unit &w) { return w.m0 + (int)rank * kRows + quarter * 32; };
         auto row_scale = [&](const Unit &w) {
             const int m = first_row(w) + lane;
-            return m < shape.x.M ? out.sa[m] : 0.f;
+            return m < shape.x.M ? ld_behind_f32(out.sa + m) : 0.f;
         };
         Unit next;
         bool more = unit_at<FORM>(0, shape, ncol, &next);
@@ -685,7 +685,7 @@ Plan plan_tiles(int M, int N, bool gated, int step, int slabs)
 // Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
 template <typename T>
 __global__ void __launch_bounds__(256)
-join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n)
+join_kernel(const float *part, T *c0, T *c1, int parts, long long n)
 {
     grid_release();
     grid_wait();
@@ -693,11 +693,27 @@ join_kernel(const float *__restrict__ part, T *c0, T *c1, int parts, long long n
     if (at >= n) return;
     const float *src = part + (size_t)blockIdx.y * parts * n + at;
     float r[8] = {};
-    for (int p = 0; p < parts; ++p, src += n) {
-        const float4 a = *reinterpret_cast<const float4 *>(src);
-        const float4 b = *reinterpret_cast<const float4 *>(src + 4);
-        r[0] += a.x, r[1] += a.y, r[2] += a.z, r[3] += a.w;
-        r[4] += b.x, r[5] += b.y, r[6] += b.z, r[7] += b.w;
+    // two parts' loads in flight (with four, at 80 registers, the CTAs do not fit beside those of the
+    // kernel ahead); the sum in the parts' order
+    for (int p = 0; p < parts; p += 2, src += 2 * n) {
+        uint4 v[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p + i < parts) {
+                v[i][0] = ld_behind_v4(src + i * n);
+                v[i][1] = ld_behind_v4(src + i * n + 4);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p + i < parts) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    r[4 * h] += __uint_as_float(v[i][h].x);
+                    r[4 * h + 1] += __uint_as_float(v[i][h].y);
+                    r[4 * h + 2] += __uint_as_float(v[i][h].z);
+                    r[4 * h + 3] += __uint_as_float(v[i][h].w);
+                }
+            }
     }
     *reinterpret_cast<uint4 *>((blockIdx.y ? c1 : c0) + at) =
         make_uint4(pack2<T>(r[0], r[1]), pack2<T>(r[2], r[3]), pack2<T>(r[4], r[5]),
