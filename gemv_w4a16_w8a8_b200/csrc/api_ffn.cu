@@ -18,6 +18,11 @@ qg_status launched(cudaError_t e)
 }
 
 constexpr int kMaxInt8K = 131072;      // 128 * 128 * K < 2^31 below it
+// Rows and columns of the products: their kernels and plans round sizes up to whole tiles, and step
+// past the last one by less than 4096, in int arithmetic.
+constexpr int kMaxSize = 0x7fffffff - 4095;
+
+bool too_large(int M, int N, int K) { return M > kMaxSize || N > kMaxSize || K > kMaxSize; }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
@@ -57,7 +62,7 @@ qg_status qgemm_w8a8_scaled(const int8_t *A, const int8_t *W, const float *a_sca
 {
     if (!A || !W || !a_scales || !w_scales || !C || M <= 0 || N <= 0 || K <= 0 || bad_dtype(dtype))
         return QG_ERR_INVALID_ARG;
-    if (K % 16 || K >= kMaxInt8K) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || K >= kMaxInt8K || too_large(M, N, K)) return QG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(A, 16) || !aligned(W, 16) || !aligned(C, 16) || !aligned(a_scales, 4) ||
         !aligned(w_scales, 4) || !aligned(bias, 2))
         return QG_ERR_ALIGNMENT;
@@ -76,7 +81,7 @@ qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
     if (!A || !Wg || !Wu || !a_scales || !g_scales || !u_scales || !H || M <= 0 || F <= 0 ||
         K <= 0 || bad_dtype(dtype) || bad_act(act))
         return QG_ERR_INVALID_ARG;
-    if (K % 16 || K >= kMaxInt8K) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || K >= kMaxInt8K || too_large(M, F, K)) return QG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(A, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(H, 16) ||
         !aligned(a_scales, 4) || !aligned(g_scales, 4) || !aligned(u_scales, 4))
         return QG_ERR_ALIGNMENT;
@@ -95,7 +100,7 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
     if (!X || !Wg || !Wu || !H || !G != !U || M <= 0 || F <= 0 || K <= 0 || bad_dtype(dtype) ||
         bad_act(act))
         return QG_ERR_INVALID_ARG;
-    if (K % 8) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 8 || too_large(M, F, K)) return QG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(H, 16) ||
         !aligned(G, 16) || !aligned(U, 16))
         return QG_ERR_ALIGNMENT;
@@ -109,7 +114,7 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
 
 size_t qgemm_dense_gated_backward_workspace_bytes(int M, int F, int K)
 {
-    if (M <= 0 || F <= 0 || K <= 0 || K % 8) return 0;
+    if (M <= 0 || F <= 0 || K <= 0 || K % 8 || too_large(M, F, K)) return 0;
     return backward_bytes(plan_gated_backward(M, F, K), M, F, K);
 }
 
@@ -121,7 +126,7 @@ qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *
     if (!dH || !X || !Wg || !Wu || !G || !U || !dWg != !dWu || (!dX && !dWg) || M <= 0 || F <= 0 ||
         K <= 0 || bad_dtype(dtype) || bad_act(act) || !workspace)
         return QG_ERR_INVALID_ARG;
-    if (K % 8) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 8 || too_large(M, F, K)) return QG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(dH, 16) || !aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) ||
         !aligned(G, 16) || !aligned(U, 16) || !aligned(dX, 16) || !aligned(dWg, 16) ||
         !aligned(dWu, 16) || !aligned(workspace, 256))

@@ -287,10 +287,12 @@ qg_status qgemm_dense_f16(const void *A, const void *W, void *C, int M, int N, i
 /* ---- 8-bit activations with scales; the gated feed-forward block ------------------------------ */
 
 /*
- * The entry points of this section choose their kernels by themselves (no pinned configurations) and
- * take any M, N and F. Their results are the same bit for bit from run to run. Consecutive calls on
- * a stream overlap one call's set-up with the end of the one before; stream order is kept. Kernels are
- * loaded at their first use on a device: make a first call of the same kind before a stream capture.
+ * The entry points of this section choose their kernels by themselves (no pinned configurations).
+ * quant_int8_tokens takes any M; the products take M, N, F and K up to 2^31 - 4096, which their tiles
+ * can round up (QG_ERR_UNSUPPORTED_SHAPE above it). Results are the same bit for bit from run to
+ * run. Consecutive calls on a stream overlap one call's set-up with the end of the one before; stream
+ * order is kept. Kernels are loaded at their first use on a device: make a first call of the same kind
+ * before a stream capture.
  */
 
 /*
