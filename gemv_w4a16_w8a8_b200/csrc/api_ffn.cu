@@ -1,5 +1,7 @@
 // C-ABI entry points of token quantisation, the scaled W8A8 matmul and the gated feed-forward
 // block: argument checks, then the launchers of ffn.cuh.
+#include <initializer_list>
+
 #include "ffn.cuh"
 
 namespace qg {
@@ -23,6 +25,28 @@ constexpr int kMaxInt8K = 131072;      // 128 * 128 * K < 2^31 below it
 constexpr int kMaxSize = 0x7fffffff - 4095;
 
 bool too_large(int M, int N, int K) { return M > kMaxSize || N > kMaxSize || K > kMaxSize; }
+
+// A buffer of a call; null where the call has none
+struct Buffer {
+    const void *p;
+    size_t bytes;
+};
+
+// Whether an output shares memory with an input or with another output
+bool overlap(std::initializer_list<Buffer> outputs, std::initializer_list<Buffer> inputs)
+{
+    auto meet = [](const Buffer &a, const Buffer &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && (x < y ? y - x < a.bytes : x - y < b.bytes);
+    };
+    for (const Buffer *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Buffer &i : inputs)
+            if (meet(*o, i)) return true;
+        for (const Buffer *q = o + 1; q != outputs.end(); ++q)
+            if (meet(*o, *q)) return true;
+    }
+    return false;
+}
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
@@ -49,6 +73,8 @@ qg_status quant_int8_tokens(const void *X, int8_t *Q, float *scales, int M, int 
     if (!X || !Q || !scales || M <= 0 || K <= 0 || bad_dtype(dtype)) return QG_ERR_INVALID_ARG;
     if (K % 8) return QG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(X, 16) || !aligned(Q, 16) || !aligned(scales, 4)) return QG_ERR_ALIGNMENT;
+    const size_t mk = (size_t)M * K;
+    if (overlap({{Q, mk}, {scales, (size_t)M * 4}}, {{X, mk * 2}})) return QG_ERR_INVALID_ARG;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);
@@ -66,6 +92,10 @@ qg_status qgemm_w8a8_scaled(const int8_t *A, const int8_t *W, const float *a_sca
     if (!aligned(A, 16) || !aligned(W, 16) || !aligned(C, 16) || !aligned(a_scales, 4) ||
         !aligned(w_scales, 4) || !aligned(bias, 2))
         return QG_ERR_ALIGNMENT;
+    if (overlap({{C, (size_t)M * N * 2}},
+                {{A, (size_t)M * K}, {W, (size_t)N * K}, {a_scales, (size_t)M * 4},
+                 {w_scales, (size_t)N * 4}, {bias, (size_t)N * 2}}))
+        return QG_ERR_INVALID_ARG;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);
@@ -85,6 +115,10 @@ qg_status qgemm_w8a8_gated(const int8_t *A, const int8_t *Wg, const int8_t *Wu,
     if (!aligned(A, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(H, 16) ||
         !aligned(a_scales, 4) || !aligned(g_scales, 4) || !aligned(u_scales, 4))
         return QG_ERR_ALIGNMENT;
+    if (overlap({{H, (size_t)M * F * 2}},
+                {{A, (size_t)M * K}, {Wg, (size_t)F * K}, {Wu, (size_t)F * K},
+                 {a_scales, (size_t)M * 4}, {g_scales, (size_t)F * 4}, {u_scales, (size_t)F * 4}}))
+        return QG_ERR_INVALID_ARG;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);
@@ -104,6 +138,9 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
     if (!aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(H, 16) ||
         !aligned(G, 16) || !aligned(U, 16))
         return QG_ERR_ALIGNMENT;
+    const size_t mf = (size_t)M * F * 2, fk = (size_t)F * K * 2;
+    if (overlap({{H, mf}, {G, mf}, {U, mf}}, {{X, (size_t)M * K * 2}, {Wg, fk}, {Wu, fk}}))
+        return QG_ERR_INVALID_ARG;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);
@@ -132,7 +169,12 @@ qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *
         !aligned(dWu, 16) || !aligned(workspace, 256))
         return QG_ERR_ALIGNMENT;
     const GradPlan plan = plan_gated_backward(M, F, K);
-    if (workspace_bytes < backward_bytes(plan, M, F, K)) return QG_ERR_SCRATCH_TOO_SMALL;
+    const size_t need = backward_bytes(plan, M, F, K);
+    if (workspace_bytes < need) return QG_ERR_SCRATCH_TOO_SMALL;
+    const size_t mf = (size_t)M * F * 2, mk = (size_t)M * K * 2, fk = (size_t)F * K * 2;
+    if (overlap({{dX, mk}, {dWg, fk}, {dWu, fk}, {workspace, need}},
+                {{dH, mf}, {X, mk}, {Wg, fk}, {Wu, fk}, {G, mf}, {U, mf}}))
+        return QG_ERR_INVALID_ARG;
     int sms = 0;
     unsigned int *err = nullptr;
     const qg_status s = current_device(&sms, &err);

@@ -51,7 +51,8 @@ extern "C" {
 
 typedef enum qg_status {
     QG_OK = 0,
-    QG_ERR_INVALID_ARG = 1,       /* null pointer, non-positive size, bad flag value        */
+    QG_ERR_INVALID_ARG = 1,       /* null pointer, non-positive size, bad flag value, an
+                                     output that overlaps another buffer of the call      */
     QG_ERR_ALIGNMENT = 2,         /* a pointer is not aligned as required                  */
     QG_ERR_UNSUPPORTED_SHAPE = 3, /* K or group_size violates the divisibility rules       */
     QG_ERR_CUDA = 4,              /* a CUDA runtime call or a kernel launch failed          */
@@ -289,10 +290,11 @@ qg_status qgemm_dense_f16(const void *A, const void *W, void *C, int M, int N, i
 /*
  * The entry points of this section choose their kernels by themselves (no pinned configurations).
  * quant_int8_tokens takes any M; the products take M, N, F and K up to 2^31 - 4096, which their tiles
- * can round up (QG_ERR_UNSUPPORTED_SHAPE above it). Results are the same bit for bit from run to
- * run. Consecutive calls on a stream overlap one call's set-up with the end of the one before; stream
- * order is kept. Kernels are loaded at their first use on a device: make a first call of the same kind
- * before a stream capture.
+ * can round up (QG_ERR_UNSUPPORTED_SHAPE above it). What a call writes, its workspace included, may
+ * overlap neither what it reads nor other things that it writes (QG_ERR_INVALID_ARG). Results are the
+ * same bit for bit from run to run. Consecutive calls on a stream overlap one call's set-up with the
+ * end of the one before; stream order is kept. Kernels are loaded at their first use on a device: make
+ * a first call of the same kind before a stream capture.
  */
 
 /*
@@ -351,8 +353,8 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
  * dX may be NULL, and so may dWg and dWu together; what is NULL is not computed.
  * workspace: caller-owned device memory, 256-byte aligned, at least
  * qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes, contents on entry and after the
- * call of no meaning. Calls that share a workspace must not overlap on the GPU. Outputs must
- * not overlap inputs. Requires K % 8 == 0; every pointer 16-byte aligned.
+ * call of no meaning. Calls that share a workspace must not overlap on the GPU.
+ * Requires K % 8 == 0; every pointer 16-byte aligned.
  */
 qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu,
                                      const void *G, const void *U, void *dX, void *dWg, void *dWu,
