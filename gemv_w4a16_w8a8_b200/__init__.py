@@ -531,6 +531,31 @@ def _current(index):
     return _torch()._C._cuda_getCurrentRawStream(index)
 
 
+_no_gradient = None
+
+
+def _cut(what, hint, out, *inputs):
+    """`out` with a node that stands where its autograd graph would: the calls record none, and a
+    backward pass that comes to the node raises, instead of leaving `inputs` without gradients."""
+    global _no_gradient
+    torch = _torch()
+    if not torch.is_grad_enabled():
+        return out
+    if _no_gradient is None:
+        class NoGradient(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, message, out, *inputs):
+                ctx.message = message
+                return out.detach()
+
+            @staticmethod
+            def backward(ctx, *grads):
+                raise RuntimeError(ctx.message)
+
+        _no_gradient = NoGradient
+    return _no_gradient.apply(f"{what} has no gradient in autograd{hint}", out, *inputs)
+
+
 def quant_int8_tokens(X, Q=None, scales=None, stream=None):
     """X fp16/bf16 [M,K] -> (Q int8 [M,K], scales fp32 [M]): amax = max |x| of the token,
     scale = amax / 127, code = rint(x * (127 / amax)) (rule in include/qgemm.h)."""
@@ -549,6 +574,8 @@ def quant_int8_tokens(X, Q=None, scales=None, stream=None):
                                  _operand(scales, torch.float32, (M,), "scales", dev), M, K, dt,
                                  _current(dev))
     _check(st, "quant_int8_tokens")
+    if X.requires_grad:
+        scales = _cut("quant_int8_tokens", "", scales, X)
     return Q, scales
 
 
@@ -575,6 +602,8 @@ def qgemm_w8a8_scaled(A, W, a_scales, w_scales, bias=None, C=None, out_dtype=Non
         None if bias is None else _operand(bias, out_dtype, (N,), "bias", dev),
         _operand(C, out_dtype, (M, N), "C", dev), M, N, K, dt, _current(dev))
     _check(st, "qgemm_w8a8_scaled")
+    if a_scales.requires_grad or w_scales.requires_grad or (bias is not None and bias.requires_grad):
+        C = _cut("qgemm_w8a8_scaled", "", C, a_scales, w_scales, bias)
     return C
 
 
@@ -603,6 +632,8 @@ def qgemm_w8a8_gated(A, Wg, Wu, a_scales, g_scales, u_scales, H=None, act: str =
         _operand(u_scales, torch.float32, (F,), "u_scales", dev),
         _operand(H, out_dtype, (M, F), "H", dev), M, F, K, code, dt, _current(dev))
     _check(st, "qgemm_w8a8_gated")
+    if a_scales.requires_grad or g_scales.requires_grad or u_scales.requires_grad:
+        H = _cut("qgemm_w8a8_gated", "", H, a_scales, g_scales, u_scales)
     return H
 
 
@@ -610,7 +641,11 @@ def qgemm_dense_gated(X, Wg, Wu, H=None, G=None, U=None, act: str = "silu",
                       save_preact: bool = False, stream=None):
     """X [M,K]; Wg, Wu [F,K], all fp16 or all bf16 -> H [M,F] = act(X Wg^T) * (X Wu^T). With
     save_preact, or with G and U given, returns (H, G, U): the pre-activations that
-    qgemm_dense_gated_backward reads. act: silu, gelu or gelu_tanh."""
+    qgemm_dense_gated_backward reads. act: silu, gelu or gelu_tanh.
+
+    No autograd graph is recorded: call it and qgemm_dense_gated_backward from the forward and
+    backward of a torch.autograd.Function. (Outside of one, a backward pass that comes to the
+    result of operands that require gradients raises RuntimeError.)"""
     torch = _torch()
     dtype = getattr(X, "dtype", None)
     dt, code = _half_type(dtype, "X"), _activation(act)
@@ -633,6 +668,11 @@ def qgemm_dense_gated(X, Wg, Wu, H=None, G=None, U=None, act: str = "silu",
         _operand(G, dtype, (M, F), "G", dev) if save else None,
         _operand(U, dtype, (M, F), "U", dev) if save else None, M, F, K, code, dt, _current(dev))
     _check(st, "qgemm_dense_gated")
+    if X.requires_grad or Wg.requires_grad or Wu.requires_grad:
+        hint = ": use qgemm_dense_gated_backward in a torch.autograd.Function"
+        H = _cut("qgemm_dense_gated", hint, H, X, Wg, Wu)
+        if save:
+            G, U = (_cut("qgemm_dense_gated", hint, t, X, Wg, Wu) for t in (G, U))
     return (H, G, U) if save else H
 
 
