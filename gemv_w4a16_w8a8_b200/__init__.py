@@ -510,7 +510,11 @@ def _activation(act):
 
 def _elsewhere(t, stream):
     """Whether a call on tensor t is for another stream, or another device, than the current one."""
-    return stream is not None or t.get_device() != _torch()._C._cuda_getDevice()
+    if stream is not None:
+        return True
+    torch = _torch()
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return t.get_device() != current()
 
 
 def _scope(t, stream):
@@ -527,8 +531,11 @@ def _scope(t, stream):
 
 
 def _current(index):
-    """Handle of the device's current stream (2 us cheaper than the Stream object around it)."""
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    """Handle of the device's current stream (by torch's shortcut, where it has it: 2 us cheaper than
+    the Stream object around it)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
 
 
 _no_gradient = None
