@@ -293,8 +293,8 @@ qg_status qgemm_dense_f16(const void *A, const void *W, void *C, int M, int N, i
  * can round up (QG_ERR_UNSUPPORTED_SHAPE above it). What a call writes, its workspace included, may
  * overlap neither what it reads nor other things that it writes (QG_ERR_INVALID_ARG). Results are the
  * same bit for bit from run to run. Consecutive calls on a stream overlap one call's set-up with the
- * end of the one before; stream order is kept. Kernels are loaded at their first use on a device: make
- * a first call of the same kind before a stream capture.
+ * end of the one before; stream order is kept. Any call may be captured into a graph, the first of a
+ * process too.
  */
 
 /*
