@@ -8,9 +8,6 @@ namespace qg {
 namespace {
 
 constexpr int kThreads = 256;
-// Up to here the few-token kernel without asking the estimates: the weights' stream is the bound (at
-// 100 tokens, 512 to 11008 columns by 2048 to 11008: 6 to 36 us against 9 to 48 us of the tiles).
-constexpr int kFewTokens = 64;
 
 // dG = dH U act'(G), dU = dH act(G), rounded to 16 bits for the tensor cores (the products that
 // read them sum in fp32; the rounding is as large as that of the gradients themselves). Rows of Fp
@@ -130,33 +127,11 @@ template <typename T, int ACT> cudaError_t run_grad_act(const GatedGrad &p, cuda
 
 } // namespace
 
-GradPlan plan_gated_backward(int M, int F, int K)
-{
-    GradPlan p = {};
-    p.w = grad_tiles(M, F, K, false, true);
-    p.few = M <= kFewTokens;
-    if (p.few) return p;
-    p.x = grad_tiles(M, F, K, true, false);
-    const GradTiles both = grad_tiles(M, F, K, true, true);
-    p.together = both.us < p.x.us + p.w.us;
-    p.few = small_dx_us(M, F, K) + p.w.us < (p.together ? both.us : p.x.us + p.w.us);
-    if (p.few) p.together = false;
-    else if (p.together) p.x = p.w = both;
-    return p;
-}
-
-size_t grad_part_bytes(const GradPlan &p, int M, int F, int K)
-{
-    size_t n = p.w.parts_w > 1 ? (size_t)p.w.parts_w * 2 * F * K : 0;
-    if (!p.few && p.x.parts_x > 1) n += (size_t)p.x.parts_x * M * K;
-    return n * 4;
-}
-
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const int slabs = (p.K + 127) / 128;
     const bool gated = p.W1 != nullptr;
-    if (p.M <= kFewTokens || small_us(p.M, p.N, gated, slabs) < tile_us(p.M, p.N, gated, true, slabs))
+    if (few_tokens(p.M, p.N, gated, true, slabs))
         return launch_small_scaled(p, err, stream);
     return launch_tile_scaled(p, err, stream);
 }
@@ -164,7 +139,7 @@ cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaSt
 cudaError_t launch_dense_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream)
 {
     const int slabs = (p.K + 63) / 64;
-    if (p.M <= kFewTokens || small_us(p.M, p.F, true, slabs) < tile_us(p.M, p.F, true, false, slabs))
+    if (few_tokens(p.M, p.F, true, false, slabs))
         return launch_small_gated(p, err, stream);
     return launch_tile_gated(p, err, stream);
 }

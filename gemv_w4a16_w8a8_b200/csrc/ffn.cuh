@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "ffn_plan.cuh"
 
 namespace qg {
 
@@ -210,18 +211,6 @@ struct GatedProblem {       // 16-bit operands, forward
     void *H, *G, *U;
     int M, F, K, act, dtype;
 };
-// Tile width and parts of the reductions of a launch of gradient tiles; us: estimate for a B200
-struct GradTiles {
-    int bn, parts_x, parts_w;
-    double us;
-};
-// How the gradients are computed: by the sizes alone, not by what is asked for, so that dX or the
-// weights' gradients by themselves are those of the whole call, bit for bit.
-struct GradPlan {
-    bool few;               // dX by the few-token kernel, only the weights' gradients by tiles
-    bool together;          // tiles of dX and of the weights' gradients in one launch
-    GradTiles x, w;
-};
 struct GatedGrad {          // backward; dG, dU and part live in the caller's workspace
     const void *dH, *X, *Wg, *Wu, *G, *U;
     void *dX, *dWg, *dWu, *dG, *dU;
@@ -236,20 +225,13 @@ cudaError_t launch_quant_int8_tokens(const void *X, int8_t *Q, float *scales, in
 cudaError_t launch_w8a8_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_dense_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_gated_backward(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
-GradPlan plan_gated_backward(int M, int F, int K);
-size_t grad_part_bytes(const GradPlan &plan, int M, int F, int K);
 
-// Large tiles (ffn_tile.cu) and few tokens (ffn_small.cu): each takes any sizes. The estimates, in
-// microseconds, choose between them; slabs: 128-byte steps of the reduction.
+// Large tiles (ffn_tile.cu) and few tokens (ffn_small.cu): each takes any sizes, ffn_plan.cuh chooses.
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_tile_grad(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
-double tile_us(int M, int N, bool gated, bool i8, int slabs);
-GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw);
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStream_t stream);
 cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t stream);
-double small_us(int M, int N, bool gated, int slabs);
-double small_dx_us(int M, int F, int K);
 
 } // namespace qg

@@ -60,6 +60,4 @@ template <bool I8, typename T> bool map_of(CUtensorMap *m, const Matrix &x, int 
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
 } // namespace qg

@@ -36,33 +36,16 @@
 namespace qg {
 namespace {
 
-enum Form { kScaled, kGated, kDx };
+using namespace few;
 
 constexpr int kThreads = 192;          // warps 0-3 accumulator and output, 4 TMA, 5 MMA
 constexpr int kOutThreads = 128;
-constexpr int kTokens = 128, kSlab = 128, kMmaM = 128;
-constexpr int kWeightMajor = 64;       // up to so many tokens the weights are the MMA's M side
-constexpr int kRingBytes = 108 * 1024;
-constexpr int kMaxStages = 16;
 
 // after the ring: 8 rows that no copy fills, token scales, barriers, TMEM address and abort flag
 constexpr int kScaleOff = kRingBytes + 8 * kSlab, kBarOff = kScaleOff + kTokens * 4;
 constexpr int kBars = 2 * kMaxStages + 1;
 constexpr int kSmem = 1024 + kBarOff + kBars * 8 + 16;
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
-
-struct Shape {
-    int M, N;               // tokens; columns of the result
-    int cols;               // result columns of a tile, a multiple of 4
-    int second;             // first row of up in a slab, a multiple of 8 (kGated)
-    int used;               // weight rows in a slab that reach a result
-    int slab_rows;          // weight rows in a slab, a multiple of 8
-    int box_tokens;         // token rows in a slab, a multiple of 8
-    int stages;
-    int pitch;              // words a token of a partial tile: 4 x odd, no bank conflicts
-    int seg_slabs, slabs;   // slabs of the reduction: of one product, of all
-    int act;
-};
 
 struct Out {
     void *c0, *c1, *c2;
@@ -401,81 +384,6 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 
 // ---- host side -------------------------------------------------------------------------------------
 
-int round_up(int a, int b) { return ceil_div(a, b) * b; }
-
-// Stages of the ring: its bytes, and the whole blocks of 128 rows that the MMA reads from the last
-// slab of the M side.
-int stages_of(int used, int box, int M)
-{
-    const int w = round_up(used, 8) * kSlab, x = box * kSlab;
-    int st = std::min(kMaxStages, kRingBytes / (w + x));
-    const bool wm = M <= kWeightMajor;
-    const int first = wm ? w : x, read = wm ? round_up(used, kMmaM) * kSlab : kMmaM * kSlab;
-    while (st > 2 && (st - 1) * first + read > kRingBytes) --st;
-    return st;
-}
-
-struct Plan {
-    int cols, parts;
-    double us;                // estimate for a B200
-};
-
-// Clusters of 1, 2, 4 and 8 CTAs that run at once on a B200 with one CTA an SM (larger clusters
-// leave SMs of a partly filled processing cluster idle) and with two.
-constexpr int kClusters[2][4] = {{148, 74, 33, 15}, {296, 148, 71, 33}};
-
-// Columns of a tile and parts of the reduction: for every cluster size and one or two CTAs an SM,
-// the columns that divide the weights evenly over the clusters that run at once (more waves of them
-// if a tile's columns would not fit), by the estimated time of
-//   - a slab: its MMAs with their waits (0.29 us of one CTA on an SM, 0.40 us of two CTAs together;
-//     more with a second block or a wide N side), what L2 delivers to an SM (115 GB/s), or the
-//     memory's 2 us over the slabs in flight;
-//   - the stream: the slabs of a CTA against HBM, the two slowing each other near balance;
-//   - joining: a barrier, and partial tiles through shared memory at 35 GB/s (60 GB/s unsplit).
-// Times in us of columns x parts, measured over a sweep: one token, 11008 gate and up columns, 4096
-// deep, 76x2: 17.1, 76x1: 17.8, 40x1: 17.8, 64x1: 19.1, 128x1: 19.4; 16 tokens in 16 bits, 76x2:
-// 30.6, 40x1: 32.7, 64x1: 33.4, 76x1: 34.7; 128 tokens, 4096 columns, 128x4: 9.0, 128x8: 11.5,
-// 64x2: 10.6.
-Plan plan_small(int form, int M, int N, int slabs)
-{
-    const int tiles_t = ceil_div(M, kTokens), box = round_up(std::min(M, kTokens), 8);
-    const int halves = form == kGated ? 2 : 1;
-    const int grain = form == kDx ? 64 : 4;
-    // the MMA's 256 rows; and the partial tile fits in the ring
-    int most = 256 / halves / 8 * 8;
-    while (most > grain && (most * halves + 8) * std::min(M, kTokens) * 4 > kRingBytes) most -= 8;
-    most = std::max(grain, most / grain * grain);
-    Plan best{grain, 1, 1e30};
-    for (int per_sm = 1; per_sm <= 2; ++per_sm)
-        for (int i = 0; i < 4; ++i) {
-            const int parts = 1 << i, slots = kClusters[per_sm - 1][i];
-            if (parts > 1 && slabs < 4 * parts) break;
-            // even columns over the fewest whole waves
-            const long long least = (long long)ceil_div(N, most) * tiles_t;
-            const long long waves = (least + slots - 1) / slots;
-            const long long tiles = std::max(1LL, slots * waves / tiles_t);
-            const int cols = round_up((int)((N + tiles - 1) / tiles), grain);
-            const long long ctas = (long long)ceil_div(N, cols) * tiles_t * parts;
-            const double on_sm = std::max(1.0, std::min(2.0, std::ceil(ctas / 148.0)));
-            const double rounds = std::max(1.0, ctas / ((double)kClusters[1][i] * parts));
-            const int used = form == kGated ? round_up(cols, 8) + cols : cols;
-            const int tokens = std::min(M, kTokens);
-            const int blocks = M <= kWeightMajor ? ceil_div(used, kMmaM) : 1;
-            const double mma = on_sm < 2 ? (blocks > 1 ? 0.40 : (used > 128 ? 0.35 : 0.29))
-                                         : (blocks > 1 ? 0.50 : 0.40 * std::max(1.0, used / 170.0));
-            const double slab = std::max({mma, on_sm * (used + box) * kSlab / 115e3,
-                                          2.0 / stages_of(used, box, M)});
-            const double sm = ceil_div(slabs, parts) * slab * rounds;
-            const double hbm = (double)slabs * kSlab * ((double)N * halves + M) / 6.4e6;
-            const double stream = std::sqrt(std::sqrt(sm * sm * sm * sm + hbm * hbm * hbm * hbm));
-            const double tile = on_sm * tokens * used * 4.0;
-            const double join = parts > 1 ? 0.5 + 0.15 * parts + tile / 35e3 : tile / 60e3;
-            const double us = 2.5 + stream + join * rounds;
-            if (us < best.us) best = Plan{cols, parts, us};
-        }
-    return best;
-}
-
 template <int FORM, bool I8, typename T, bool WM>
 cudaError_t launch_plan(const Matrix &w0, const Matrix &w1, const Matrix &x0, const Matrix &x1,
                         Shape shape, const Out &out, unsigned int *err, cudaStream_t stream)
@@ -495,15 +403,7 @@ cudaError_t launch_plan(const Matrix &w0, const Matrix &w1, const Matrix &x0, co
         }
     }
     const Plan plan = plan_small(FORM, shape.M, shape.N, shape.slabs);
-    shape.cols = plan.cols;
-    shape.second = FORM == kGated ? round_up(plan.cols, 8) : 0;
-    const int used = shape.used = shape.second + plan.cols;
-    shape.box_tokens = round_up(std::min(shape.M, kTokens), 8);
-    shape.pitch = used / 4 % 2 ? used : used + 4;
-    shape.slab_rows = round_up(used, 8);
-    shape.stages = stages_of(used, shape.box_tokens, shape.M);
-    if (std::min(shape.M, kTokens) * shape.pitch * 4 > kRingBytes || used > 256 || shape.stages < 2)
-        return cudaErrorInvalidConfiguration;
+    if (!lay_out(&shape, plan.cols, FORM)) return cudaErrorInvalidConfiguration;
     const long long tiles = (long long)ceil_div(shape.N, plan.cols) * ceil_div(shape.M, kTokens);
     if (tiles * plan.parts > 0x7fffffffLL) return cudaErrorInvalidValue;
     // a slab's box: the tile's columns of a weight matrix, or 64 rows of the reduction for kDx
@@ -528,25 +428,7 @@ cudaError_t launch_small(const Matrix &w0, const Matrix &w1, const Matrix &x0, c
     return launch_plan<FORM, I8, T, false>(w0, w1, x0, x1, shape, out, err, stream);
 }
 
-Shape shape_of(int M, int N, int seg_slabs, int segs, int act)
-{
-    Shape s = {};
-    s.M = M;
-    s.N = N;
-    s.seg_slabs = seg_slabs;
-    s.slabs = segs * seg_slabs;
-    s.act = act;
-    return s;
-}
-
 } // namespace
-
-double small_us(int M, int N, bool gated, int slabs)
-{
-    return plan_small(gated ? kGated : kScaled, M, N, slabs).us;
-}
-
-double small_dx_us(int M, int F, int K) { return plan_small(kDx, M, K, 2 * ceil_div(F, 64)).us; }
 
 cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {

@@ -47,16 +47,14 @@
 namespace qg {
 namespace {
 
-enum Form { kScaled, kGated, kDx, kDw, kBoth };
+using namespace tile;
 
 constexpr bool is_grad(int form) { return form >= kDx; }
 
 constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
-constexpr int kTileM = 256, kRows = 128;       // rows of the result: of a pair, of a CTA
-constexpr int kMaxBn = 256;
+constexpr int kRows = kTileM / 2;              // rows of the result of a CTA
 constexpr int kSlab = 128;                     // bytes of the reduction per stage (K-major)
-constexpr int kRasterM = 8;                    // row tiles per raster group (4, 16: no faster)
 
 // Shared memory: stages of a CTA's 128 rows x 128 B and up to 128 rows x 128 B of the other
 // operand, then for each epilogue warp 32 rows x 64 B of results and 64 column factors.
@@ -72,78 +70,12 @@ constexpr int total = 1024 + bar_off + nbars * 8 + 16;
 static_assert(total <= 227 * 1024, "shared memory");
 } // namespace ring
 
-// One product of a launch (gradients: dX, and the two weights' gradients together)
-struct Work {
-    int M, tiles_m;         // the result's rows, and tiles of them
-    int slabs;              // slabs of the reduction
-    int parts, part_slabs;  // parts of the reduction and slabs of each (the last may have fewer)
-    int units;              // results x tiles x parts; 0: not computed
-};
-
-struct Shape {
-    int N, tiles_n;         // the result's columns (of H for kGated)
-    int bn;                 // the MMA's N: columns of a tile (kGated: of gate and up together)
-    int seg_slabs;          // slabs of one of dX's two products
-    int act;
-    Work x, w;              // the product, or dX; the weights' gradients
-    int full, rem;          // units of x: `full` a pair, one more for the first `rem` pairs
-    int extra;              // tiles of w that pairs with one tile of x less take for it
-};
-
 struct Out {
     void *c0, *c1, *c2;                 // C / H, G, U / dX, dWg, dWu
     float *part_x, *part_w;             // fp32 partial sums [result][part][M][N]
     const float *sa, *sw, *sw1;
     const void *bias;
 };
-
-struct Unit {
-    int which, m0, n0, part, s0, ns;    // result, origin of the tile, part, first slab, slabs
-};
-
-// Tiles in groups of kRasterM row tiles, rows fastest: the pairs at work at one time share a block
-// of about kRasterM x 9 tiles whose operands stay in L2.
-__device__ __forceinline__ Unit unit_of(int u, const Work &k, int tiles_n, int ncol)
-{
-    Unit w;
-    w.part = u % k.parts;
-    int t = u / k.parts;
-    const int per = k.tiles_m * tiles_n;
-    w.which = t / per;
-    t -= w.which * per;
-    const int group = t / (kRasterM * tiles_n);
-    const int first = group * kRasterM;
-    const int gm = min(kRasterM, k.tiles_m - first);
-    t -= group * kRasterM * tiles_n;
-    w.m0 = (first + t % gm) * kTileM;
-    w.n0 = (t / gm) * ncol;
-    w.s0 = w.part * k.part_slabs;
-    w.ns = min(k.part_slabs, k.slabs - w.s0);
-    return w;
-}
-
-// The j-th unit of this pair, in *w; false behind its last one.
-template <int FORM>
-__device__ __forceinline__ bool unit_at(int j, const Shape &s, int ncol, Unit *w)
-{
-    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    const int u = j * pairs + pair;
-    if (FORM != kDw && u < s.x.units) {
-        *w = unit_of(u, s.x, s.tiles_n, ncol);
-        return true;
-    }
-    if constexpr (FORM != kDw && FORM != kBoth) return false;
-    const int i = j - s.full - (pair < s.rem ? 1 : 0);
-    int v = i * pairs + pair;
-    if (s.rem > 0) {
-        if (pair >= s.rem && i < s.extra) v = i * (pairs - s.rem) + pair - s.rem;
-        else v += s.extra * (pairs - s.rem) - (pair >= s.rem ? s.extra * pairs : 0);
-    }
-    if (v >= s.w.units) return false;
-    *w = unit_of(v, s.w, s.tiles_n, ncol);
-    w->which += 1;
-    return true;
-}
 
 // A warp's 32 rows x 64 bytes of results, staged in shared memory (16-byte piece j of row r at j ^
 // (r / 2 & 3): neither side has bank conflicts) and written as whole rows: 16 bytes a lane where
@@ -281,11 +213,14 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     auto place = [&](const Unit &w, int i) {
         return (w.s0 + i - (second(w, i) ? shape.seg_slabs : 0)) * kElems;
     };
+    auto unit_at = [&](int j, Unit *u) {
+        return tile::unit_at<FORM>(j, (int)(gridDim.x >> 1), (int)(blockIdx.x >> 1), shape, ncol, u);
+    };
     // The first slabs of the operand that is not a token's (weights, or X in the weights'
     // gradients) go to L2 before the kernels ahead on the stream have finished: what one of them
     // still writes is written in L2, so what is read behind grid_wait() is right either way.
     Unit w, w0;
-    if (warp == kTmaWarp && unit_at<FORM>(0, shape, ncol, &w0) && lane == 0) {
+    if (warp == kTmaWarp && unit_at(0, &w0) && lane == 0) {
         for (int i = 0; i < min(w0.ns, ST); ++i) {
             const int r = row_b(w0), k = place(w0, i);
             tma_prefetch_2d(map_b(w0, i), BMN ? r : k, BMN ? k : r);
@@ -303,7 +238,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         int it = 0, s = 0;
         uint32_t phase = 1;
         bool stop = false;
-        for (int j = 0; !stop && unit_at<FORM>(j, shape, ncol, &w); ++j) {
+        for (int j = 0; !stop && unit_at(j, &w); ++j) {
             const int ra = row_a(w), rb = row_b(w);
             const bool amn = a_mn(j);
             // dX: the slabs of its first product, then those of the second
@@ -358,7 +293,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         int s = 0;
         uint32_t phase = 0;
         bool stop = false;
-        for (int j = 0; !stop && unit_at<FORM>(j, shape, ncol, &w); ++j) {
+        for (int j = 0; !stop && unit_at(j, &w); ++j) {
             const int b = j & 1;
             if (!warp_wait(acce_bar(b), ((j >> 1) & 1) ^ 1, abort_flag, err)) break;
             tc_fence_after();
@@ -424,7 +359,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
             return m < shape.x.M ? ld_behind_f32(out.sa + m) : 0.f;
         };
         Unit next;
-        bool more = unit_at<FORM>(0, shape, ncol, &next);
+        bool more = unit_at(0, &next);
         float sa_next = 0.f;
         if constexpr (I8) {
             sa_next = row_scale(next);
@@ -440,7 +375,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
             const int rows = min(32, M - m);
             const int nc = min(ncol, N - w.n0);
             sa = sa_next;
-            more = unit_at<FORM>(j + 1, shape, ncol, &next);
+            more = unit_at(j + 1, &next);
             if constexpr (I8) sa_next = row_scale(next);
             bool ok = mbar_wait(accf_bar(b), (j >> 1) & 1, abort_flag, err);
             tc_fence_after();
@@ -570,15 +505,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 
 // ---- host side -------------------------------------------------------------------------------------
 
-// Tiles of w that a pair takes in place of its missing last tile of x
-int extra_tiles(const Work &x, const Work &w, int pairs)
-{
-    const int rem = x.units % pairs;
-    if (rem == 0 || w.units == 0) return 0;
-    const int fit = (x.part_slabs + w.part_slabs / 2) / w.part_slabs;
-    return std::min(fit, w.units / (pairs - rem));
-}
-
 template <int FORM, bool I8, typename T>
 cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, const Matrix &b1,
                         const Matrix &b2, Shape shape, const Out &out, unsigned int *err,
@@ -618,9 +544,7 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
     if (shape.x.units < 0 || shape.w.units < 0) return cudaErrorInvalidValue;    // beyond an int
     const long long units = (long long)shape.x.units + shape.w.units;
     pairs = (int)std::min<long long>(units, pairs);
-    shape.full = shape.x.units / pairs;
-    shape.rem = shape.x.units % pairs;
-    shape.extra = extra_tiles(shape.x, shape.w, pairs);
+    share_units(&shape, pairs);
     CUtensorMap ta0, ta1, ta2, ta3, tb0, tb1, tb2;
     // MN-major operands arrive in boxes of 64 rows
     const int b_rows = is_grad(FORM) ? 64 : shape.bn / 2;
@@ -635,51 +559,6 @@ cudaError_t launch_tile(const Matrix &a0, const Matrix &a1, const Matrix &b0, co
         return cudaErrorInvalidValue;
     return launch_dependent(kern, dim3(2 * pairs), dim3(kThreads), ring::total, 2, stream, ta0, ta1,
                             tb0, tb1, ta2, ta3, tb2, shape, out, err);
-}
-
-// Widths that the MMA of a pair takes: multiples of 32 for int8 and of 16 for 16-bit types. The
-// gradients' MN-major operands come in whole chunks of 64 values a CTA: 128 or 256 columns.
-constexpr int kStepI8 = 32, kStep16 = 16;
-constexpr int kPairs = 74;             // of a B200
-constexpr int kMaxParts = 16;
-
-Work work_of(int M, int N, int ncol, int results, int slabs, int parts)
-{
-    Work k = {};
-    k.M = M;
-    k.tiles_m = ceil_div(M, kTileM);
-    k.slabs = slabs;
-    k.part_slabs = ceil_div(slabs, parts);
-    k.parts = ceil_div(slabs, k.part_slabs);        // no empty part
-    const long long units = (long long)results * k.tiles_m * ceil_div(N, ncol) * k.parts;
-    k.units = units > 0x7fffffffLL ? -1 : (int)units;
-    return k;
-}
-
-// A slab takes 0.34 us in a wave that fills the device, nearly whatever the width: 128 columns
-// 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and L2 delivers
-// little more than 90 GB/s to an SM).
-double slab_us(int bn) { return 0.34 * (0.88 + 0.12 * bn / kMaxBn); }
-
-struct Plan {
-    int bn;
-    double us;                         // estimate for a B200
-};
-
-// Tile width of the scaled and gated products: whole waves of tiles over the CTA pairs. Fewest
-// waves win, and among them the narrower tile, whose epilogue is shorter: 2 x 43 tiles of 256
-// columns on 74 pairs, say, leave most of a second wave idle; 2 x 69 tiles of 160 take the same two
-// waves 15 % faster (509 x 11007 x 4080: 38.3 -> 32.4 us).
-Plan plan_tiles(int M, int N, bool gated, int step, int slabs)
-{
-    const long long tm = ceil_div(M, kTileM);
-    Plan best{kMaxBn, 1e30};
-    for (int bn = kMaxBn; bn >= 64; bn -= step) {
-        const long long units = tm * ceil_div(N, gated ? bn / 2 : bn);
-        const double us = 3.5 + (double)((units + kPairs - 1) / kPairs) * slabs * slab_us(bn);
-        if (us < best.us - 1e-9) best = Plan{bn, us};
-    }
-    return best;
 }
 
 // Sum of the parts in order, rounded to 16 bits: [which][part][n] -> c0, c1 [n], n a multiple of 8
@@ -730,66 +609,7 @@ cudaError_t join_parts(const float *part, void *c0, void *c1, const Work &k, int
                             static_cast<T *>(c0), static_cast<T *>(c1), k.parts, n);
 }
 
-Shape shape_of(int M, int N, int bn, int ncol, int slabs, int act)
-{
-    Shape s = {};
-    s.N = N;
-    s.tiles_n = ceil_div(N, ncol);
-    s.bn = bn;
-    s.act = act;
-    s.x = work_of(M, N, ncol, 1, slabs, 1);
-    return s;
-}
-
 } // namespace
-
-// Tile width and parts of the gradients of one launch. Parts cost their fp32 sums' way to memory and
-// back and a second kernel; they are tried while the pairs have at most two tiles each.
-GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
-{
-    const int slabs_x = 2 * ceil_div(F, 64), slabs_w = ceil_div(M, 64);
-    const int most = dx && dw ? 2 * kPairs : kPairs * 3 / 2;     // units: 256 KB of sums each
-    GradTiles best{kMaxBn, 1, 1, 1e30};
-    for (int bn = kMaxBn; bn >= kMaxBn / 2; bn /= 2) {
-        const Work x1 = work_of(M, K, bn, 1, slabs_x, 1), w1 = work_of(F, K, bn, 2, slabs_w, 1);
-        if (x1.units < 0 || w1.units < 0) continue;
-        auto consider = [&](int px, int pw) {
-            // parts keep eight slabs
-            if ((px > 1 && slabs_x < 8 * px) || (pw > 1 && slabs_w < 8 * pw)) return;
-            const long long units =
-                (dx ? (long long)x1.units * px : 0) + (dw ? (long long)w1.units * pw : 0);
-            if ((px > 1 || pw > 1) && units > most) return;
-            const Work x = dx ? (px > 1 ? work_of(M, K, bn, 1, slabs_x, px) : x1) : Work{};
-            const Work w = dw ? (pw > 1 ? work_of(F, K, bn, 2, slabs_w, pw) : w1) : Work{};
-            const int pairs = (int)std::min<long long>((long long)x.units + w.units, kPairs);
-            const int full = x.units / pairs, rem = x.units % pairs;
-            const int extra = extra_tiles(x, w, pairs);
-            long long slabs = (long long)full * x.part_slabs;
-            if (rem > 0) slabs += std::max(x.part_slabs, extra * w.part_slabs);
-            const int left = w.units - (rem > 0 ? extra * (pairs - rem) : 0);
-            slabs += (long long)ceil_div(left, pairs) * w.part_slabs;
-            double us = 3.5 + slabs * slab_us(bn) * (dx && dw ? 1.10 : 1.0);
-            if (x.parts > 1) us += 2.5 + (double)M * K * 8 * x.parts / 5e6;
-            if (w.parts > 1) us += 2.5 + (double)2 * F * K * 8 * w.parts / 5e6;
-            if (us < best.us - 1e-9)
-                best = GradTiles{bn, std::max(1, x.parts), std::max(1, w.parts), us};
-        };
-        consider(1, 1);
-        const long long least =
-            std::min(dx ? x1.units : 0x7fffffff, dw ? w1.units : 0x7fffffff);
-        for (int parts = 2; parts <= kMaxParts && least * parts <= most; ++parts) {
-            if (dx) consider(parts, 1);
-            if (dw) consider(1, parts);
-            if (dx && dw) consider(parts, parts);
-        }
-    }
-    return best;
-}
-
-double tile_us(int M, int N, bool gated, bool i8, int slabs)
-{
-    return plan_tiles(M, N, gated, i8 ? kStepI8 : kStep16, slabs).us;
-}
 
 cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaStream_t stream)
 {
@@ -832,19 +652,9 @@ cudaError_t launch_tile_grad(const GatedGrad &p, unsigned int *err, cudaStream_t
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2}, x{p.X, M, K, K * 2};
-    auto grad_shape = [&](const GradTiles &t, bool of_x, bool of_w) {
-        Shape s = {};
-        s.N = p.K;
-        s.bn = t.bn;
-        s.tiles_n = ceil_div(p.K, t.bn);
-        s.seg_slabs = ceil_div(p.F, 64);
-        if (of_x) s.x = work_of(p.M, p.K, t.bn, 1, 2 * s.seg_slabs, t.parts_x);
-        if (of_w) s.w = work_of(p.F, p.K, t.bn, 2, ceil_div(p.M, 64), t.parts_w);
-        return s;
-    };
     const bool both = plan.together && dx && dw;
-    const Shape sx = dx ? grad_shape(plan.x, true, both) : Shape{};
-    const Shape sw = grad_shape(plan.w, false, dw);
+    const Shape sx = dx ? grad_shape(plan.x, p.M, p.F, p.K, true, both) : Shape{};
+    const Shape sw = grad_shape(plan.w, p.M, p.F, p.K, false, dw);
     Out out = {};
     out.c0 = p.dX;
     out.c1 = p.dWg;
