@@ -57,7 +57,7 @@ struct Shape {
     int act;
     Work x, w;              // the product, or dX; the weights' gradients
     int full, rem;          // units of x: `full` a pair, one more for the first `rem` pairs
-    int extra;              // tiles of w that pairs with one tile of x less take for it
+    int extra;              // tiles of w that pairs with one tile of x less take for it, first of all
 };
 
 struct Unit {
@@ -95,11 +95,14 @@ QG_PLAN_FN bool unit_at(int j, int pairs, int pair, const Shape &s, int ncol, Un
         return true;
     }
     if constexpr (FORM != kDw && FORM != kBoth) return false;
-    const int i = j - s.full - (pair < s.rem ? 1 : 0);
-    int v = i * pairs + pair;
-    if (s.rem > 0) {
-        if (pair >= s.rem && i < s.extra) v = i * (pairs - s.rem) + pair - s.rem;
-        else v += s.extra * (pairs - s.rem) - (pair >= s.rem ? s.extra * pairs : 0);
+    // The weights' units go on where x's end, at the pairs that have one of x less; or `extra` rounds
+    // over those pairs alone, then rounds over all.
+    int v = u - s.x.units;
+    if (s.extra > 0) {
+        const int i = j - s.full - (pair < s.rem ? 1 : 0), lacking = pairs - s.rem;
+        if (pair < s.rem) v = i * pairs + pair + s.extra * lacking;
+        else if (i < s.extra) v = i * lacking + pair - s.rem;
+        else v = (i - s.extra) * pairs + pair + s.extra * lacking;
     }
     if (v >= s.w.units) return false;
     *w = unit_of(v, s.w, s.tiles_n, ncol);

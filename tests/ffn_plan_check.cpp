@@ -38,7 +38,7 @@ template <int FORM> static int walk(tile::Shape s, int ncol)
     const int pairs = (int)std::min<long long>(units, tile::kPairs);
     tile::share_units(&s, pairs);
     std::set<std::tuple<int, int, int, int>> seen;
-    int most = 0;
+    int most = 0, least = 1 << 30;
     for (int pair = 0; pair < pairs; ++pair) {
         tile::Unit w;
         int j = 0;
@@ -53,7 +53,11 @@ template <int FORM> static int walk(tile::Shape s, int ncol)
             CHECK(w.part < k.parts && w.ns >= 1 && w.s0 >= 0 && w.s0 + w.ns <= k.slabs, "slabs %d + %d", w.s0, w.ns);
         }
         most = std::max(most, j);
+        least = std::min(least, j);
     }
+    CHECK(least > 0, "a pair without a unit");
+    // no rounds of their own for the pairs that have a tile of dX less: units are dealt out evenly
+    if (s.extra == 0) CHECK(most - least <= 1, "%d units for a pair, %d for another", most, least);
     CHECK((long long)seen.size() == units, "%lld units, %zu done", units, seen.size());
     return most;
 }
