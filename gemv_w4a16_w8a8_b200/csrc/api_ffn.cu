@@ -55,9 +55,11 @@ int padded_f(int F) { return (F + 7) & ~7; }
 // bytes of dG (and of dU): M rows of padded_f(F) 16-bit values
 size_t grad_bytes(int M, int F) { return round256((size_t)M * padded_f(F) * 2); }
 
+constexpr size_t kScaleBytes = (kGradScale * 4 + 255) / 256 * 256;
+
 size_t backward_bytes(const GradPlan &plan, int M, int F, int K)
 {
-    return 2 * grad_bytes(M, F) + round256(grad_part_bytes(plan, M, F, K));
+    return 2 * grad_bytes(M, F) + kScaleBytes + round256(grad_part_bytes(plan, M, F, K));
 }
 
 } // namespace
@@ -180,8 +182,10 @@ qg_status qgemm_dense_gated_backward(const void *dH, const void *X, const void *
     const qg_status s = current_device(&sms, &err);
     if (s != QG_OK) return s;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint8_t *scale = ws + 2 * grad_bytes(M, F);
     const GatedGrad p{dH, X, Wg, Wu, G, U, dX, dWg, dWu, ws, ws + grad_bytes(M, F), M, F, K, act,
-                      dtype, padded_f(F), reinterpret_cast<float *>(ws + 2 * grad_bytes(M, F)), plan};
+                      dtype, padded_f(F), reinterpret_cast<float *>(scale + kScaleBytes),
+                      reinterpret_cast<float *>(scale), plan};
     return launched(launch_gated_backward(p, err, stream));
 }
 

@@ -114,9 +114,9 @@ template <int V> struct Const {
 // ------------------------------------------------------------------------------------------
 // Programmatic dependent launch. grid_wait() returns when the kernels before this one on the stream
 // have finished and their writes are visible; grid_release() lets the next kernel's CTAs start once
-// every CTA of this one has called it. The kernels without tensor cores (quantisation, elementwise
-// half of the gradients, joining of parts) release as soon as they start, the tensor-core kernels
-// when the last of their loads is on its way. Results are written, and operands read, only behind
+// every CTA of this one has called it. Quantisation, the elementwise half of the gradients and the
+// joining of parts release as soon as they start, the tensor-core kernels and the first pass of
+// fp16 gradients when the last of their loads is on its way. Results are written, and operands read, only behind
 // grid_wait(); before it the tensor-core kernels do no more than ask for their first weights to be
 // brought into L2, where a predecessor's writes to them land too. So a kernel's launch, barrier and
 // tensor-memory set-up run under the end of its predecessor, and stream order is kept: 1 to 3 us
@@ -211,12 +211,15 @@ struct GatedProblem {       // 16-bit operands, forward
     void *H, *G, *U;
     int M, F, K, act, dtype;
 };
+// fp16: the factor, and behind it the largest value that each CTA of a first pass has seen
+constexpr int kGradTops = 4 * 148, kGradScale = 4 + kGradTops;
 struct GatedGrad {          // backward; dG, dU and part live in the caller's workspace
     const void *dH, *X, *Wg, *Wu, *G, *U;
     void *dX, *dWg, *dWu, *dG, *dU;
     int M, F, K, act, dtype;
     int Fp;                 // row pitch of dG and dU in elements (a multiple of 8)
     float *part;            // partial sums, grad_part_bytes() bytes
+    float *scale;           // fp16: what the products of dG and dU are multiplied by; kGradScale floats
     GradPlan plan;
 };
 

@@ -51,6 +51,7 @@ struct Out {
     void *c0, *c1, *c2;
     const float *sa, *sw, *sw1;
     const void *bias;
+    const float *scale;     // of fp16 gradients: of what dG and dU were multiplied by
 };
 
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr)
@@ -180,7 +181,9 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
     const int n = n0 + 4 * (g0 + (ng > 0 ? (int)threadIdx.x % ng : 0));
     const int first = token0 + (ng > 0 ? (int)threadIdx.x / ng : 0);
     const bool mine = (int)threadIdx.x < ng * step && n < N;
-    float f0[4] = {}, f1[4] = {};
+    float f0[4] = {}, f1[4] = {}, back = 1.f;
+    if constexpr (FORM == kDx && std::is_same<T, __half>::value)
+        if (warp < 4) back = ld_behind_f32(out.scale);
     if (I8 && warp < 4) {
         scale_s[threadIdx.x] = (int)threadIdx.x < tokens ? ld_behind_f32(out.sa + t0 + threadIdx.x) : 0.f;
         if (mine) {
@@ -369,6 +372,7 @@ small_kernel(const __grid_constant__ CUtensorMap tm_w0, const __grid_constant__ 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     r[e] = scaled(a[e], sa, f0[e]);
+                    if constexpr (FORM == kDx) r[e] *= back;
                     if constexpr (I8) {
                         if (out.bias) r[e] = __fadd_rn(r[e], f1[e]);
                     }
@@ -435,7 +439,7 @@ cudaError_t launch_small_scaled(const ScaledProblem &p, unsigned int *err, cudaS
     const uint64_t K = p.K;
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
     const Matrix w1{p.W1 ? p.W1 : p.W, (uint64_t)p.N, K, K};
-    const Out out{p.C, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
+    const Out out{p.C, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias, nullptr};
     const Shape shape = shape_of(p.M, p.N, ceil_div(p.K, 128), 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
         if (p.W1) return launch_small<kGated, true, T>(w, w1, a, a, shape, out, err, stream);
@@ -448,7 +452,7 @@ cudaError_t launch_small_gated(const GatedProblem &p, unsigned int *err, cudaStr
     const uint64_t K = p.K, pitch = K * 2;
     const Matrix x{p.X, (uint64_t)p.M, K, pitch};
     const Matrix g{p.Wg, (uint64_t)p.F, K, pitch}, u{p.Wu, (uint64_t)p.F, K, pitch};
-    const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr};
+    const Out out{p.H, p.G, p.U, nullptr, nullptr, nullptr, nullptr, nullptr};
     const Shape shape = shape_of(p.M, p.F, ceil_div(p.K, 64), 1, p.act);
     QG_DISPATCH_16(p.dtype, T, {
         return launch_small<kGated, false, T>(g, u, x, x, shape, out, err, stream);
@@ -460,7 +464,7 @@ cudaError_t launch_small_dx(const GatedGrad &p, unsigned int *err, cudaStream_t 
     const uint64_t M = p.M, F = p.F, K = p.K;
     const Matrix dg{p.dG, M, F, (uint64_t)p.Fp * 2}, du{p.dU, M, F, (uint64_t)p.Fp * 2};
     const Matrix wg{p.Wg, F, K, K * 2}, wu{p.Wu, F, K, K * 2};
-    const Out out{p.dX, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+    const Out out{p.dX, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, p.scale};
     const Shape shape = shape_of(p.M, p.K, ceil_div(p.F, 64), 2, 0);
     QG_DISPATCH_16(p.dtype, T, {
         return launch_small<kDx, false, T>(wg, wu, dg, du, shape, out, err, stream);

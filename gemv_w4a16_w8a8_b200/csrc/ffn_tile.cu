@@ -75,6 +75,7 @@ struct Out {
     float *part_x, *part_w;             // fp32 partial sums [result][part][M][N]
     const float *sa, *sw, *sw1;
     const void *bias;
+    const float *scale;                 // of fp16 gradients: of what dG and dU were multiplied by
 };
 
 // A warp's 32 rows x 64 bytes of results, staged in shared memory (16-byte piece j of row r at j ^
@@ -360,7 +361,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         };
         Unit next;
         bool more = unit_at(0, &next);
-        float sa_next = 0.f;
+        float sa_next = 0.f, back = 1.f;
+        if constexpr (is_grad(FORM) && std::is_same<T, __half>::value) back = ld_behind_f32(out.scale);
         if constexpr (I8) {
             sa_next = row_scale(next);
             factors(next, first);
@@ -433,6 +435,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                                         __fadd_rn(__uint_as_float(v[4 * q + e]), fs[e]));
                             }
                         }
+                    }
+                    if constexpr (is_grad(FORM) && std::is_same<T, __half>::value) {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            v[q] = __float_as_uint(__uint_as_float(v[q]) * back);
                     }
                     uint32_t hw[16];
                     if constexpr (FORM == kGated) {
@@ -617,7 +624,7 @@ cudaError_t launch_tile_scaled(const ScaledProblem &p, unsigned int *err, cudaSt
     const bool gated = p.W1 != nullptr;
     const Matrix a{p.A, (uint64_t)p.M, K, K}, w{p.W, (uint64_t)p.N, K, K};
     const Matrix w1{gated ? p.W1 : p.W, (uint64_t)p.N, K, K};
-    const Out out{p.C, nullptr, nullptr, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias};
+    const Out out{p.C, nullptr, nullptr, nullptr, nullptr, p.sa, p.sw, p.sw1, p.bias, nullptr};
     const int slabs = ceil_div(p.K, 128);
     const int bn = plan_tiles(p.M, p.N, gated, kStepI8, slabs).bn;
     const Shape shape = shape_of(p.M, p.N, bn, gated ? bn / 2 : bn, slabs, p.act);
@@ -661,6 +668,7 @@ cudaError_t launch_tile_grad(const GatedGrad &p, unsigned int *err, cudaStream_t
     out.c2 = p.dWu;
     out.part_x = p.part;
     out.part_w = p.part;
+    out.scale = p.scale;
     if (!plan.few && plan.x.parts_x > 1) out.part_w += (size_t)plan.x.parts_x * p.M * p.K;
     QG_DISPATCH_16(p.dtype, T, {
         cudaError_t e = cudaSuccess;
