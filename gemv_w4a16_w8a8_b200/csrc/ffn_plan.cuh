@@ -146,9 +146,11 @@ inline Work work_of(int M, int N, int ncol, int results, int slabs, int parts)
     return k;
 }
 
-// A slab takes 0.34 us in a wave that fills the device, nearly whatever the width: 128 columns
-// 0.30, 256 columns 0.34 (the 256-row operand passes through the MMA either way, and L2 delivers
-// little more than 90 GB/s to an SM).
+// Estimate of a slab in a wave that fills the device, nearly whatever the width (the 256-row operand
+// passes through the MMA either way, and L2 delivers little more than 90 GB/s to an SM): 0.34 us at
+// 256 columns, 0.32 at 128. Measured between reductions of 4096 and 8192 int8 values: 0.33 us at 256
+// columns (72 tiles), 0.29 at 128 (64 tiles); between 8192 and 16384, with the clock lower: 0.35 and
+// 0.33.
 inline double slab_us(int bn) { return 0.34 * (0.88 + 0.12 * bn / kMaxBn); }
 
 struct Plan {
@@ -159,7 +161,9 @@ struct Plan {
 // Tile width of the scaled and gated products: whole waves of tiles over the CTA pairs. Fewest
 // waves win, and among them the narrower tile, whose epilogue is shorter: 2 x 43 tiles of 256
 // columns on 74 pairs, say, leave most of a second wave idle; 2 x 69 tiles of 160 take the same two
-// waves 15 % faster (509 x 11007 x 4080: 38.3 -> 32.4 us).
+// waves 15 % faster (509 x 11007 x 4080: 38.3 -> 32.4 us). The estimate is for comparisons: it leaves
+// out rows that are not 16-byte aligned and 3 us of the first loads and the last epilogue (24 us for
+// that call, 16.7 measured for 14.4 estimated at 2048 x 2304 x 4096).
 inline Plan plan_tiles(int M, int N, bool gated, int step, int slabs)
 {
     const long long tm = ceil_div(M, kTileM);
@@ -184,7 +188,12 @@ inline Shape shape_of(int M, int N, int bn, int ncol, int slabs, int act)
 }
 
 // Tile width and parts of the gradients of one launch. Parts cost their fp32 sums' way to memory and
-// back and a second kernel; they are tried while the pairs have at most two tiles each.
+// back and a second kernel; they are tried while the pairs have at most two tiles each. Both products
+// in one launch count a tenth more a slab: 3 to 8 % that theirs take longer, and a margin. Joined
+// against two launches, us, where the estimates choose two: 2843 x 1357 x 3888 134 against 128,
+// 2048 x 11008 x 4096 611 against 597, 2048 x 2048 x 2048 59.5 against 60.2, 512 x 11008 x 512 49
+// against 52; where they choose one: 3000 x 1500 x 696 33.1 against 48.8, 1024 x 4096 x 2048 63
+// against 68, 300 x 4096 x 512 26.7 against 28.3.
 inline GradTiles grad_tiles(int M, int F, int K, bool dx, bool dw)
 {
     const int slabs_x = 2 * ceil_div(F, 64), slabs_w = ceil_div(M, 64);

@@ -19,10 +19,11 @@
 //   kDx      dG Wg + dU Wu as one reduction over 2 F: the slabs of dG Wg, then those of dU Wu
 //   kDw      dG^T X and dU^T X: two results in one launch
 //   kBoth    kDx and kDw in one launch. dX's tiles are few and long, the weights' many and short: the
-//            pairs that get one tile of dX less than others take as many of the weights' tiles for
-//            it, then all share the rest, so that both products end together instead of leaving
-//            a partial wave each (3000 x 1500 x 700: 52 -> 37 us). Its slabs are 3 to 8 % slower
-//            (operand layouts are chosen unit by unit), so whole waves stay with two launches
+//            pairs that get one tile of dX less than others take as many whole rounds of the weights'
+//            tiles for it as fit, then all share the rest, instead of a partial wave of each product
+//            (M x F x K = 3000 x 1500 x 696: 48.8 -> 33.1 us; 1741 x 580 x 2688: 37.8 -> 29.4). Its
+//            slabs are 3 to 8 % slower (operand layouts are chosen unit by unit), so whole waves stay
+//            with two launches
 // Few tiles and a long reduction (gradients): the reduction is cut into parts that store fp32 partial
 // sums, added in order by a second kernel (no atomics: the same bits every run).
 //
@@ -33,10 +34,11 @@
 //
 // Bound: the tensor pipe. A tile of 256 columns asks an SM for 32 KB of operands per slab of 512
 // MMA cycles, about what L2 delivers to one (90 GB/s), so it reaches 75 to 80 % of the MMA's rate
-// with int8 and 80 to 92 % with 16 bits inside a wave. Device time of calls that follow one
-// another: 8192 x 11008 x 4096 bf16, G and U saved, 0.99 ms cool (1.5 PFLOP/s, 92 % of the burst
-// matmul rate) and 1.2 ms under the power cap (88 % of the sustained rate); its backward pass 2.0
-// and 2.5 ms; int8 16384^3 2.7 ms (3.2 POP/s) and 3.3 ms; int8 512 x 11008 x 4096 gated 41 us.
+// with int8 and 80 to 92 % with 16 bits inside a wave. Times on a cool GPU, and of calls that follow
+// one another until its power cap holds the clock: 8192 x 11008 x 4096 bf16, G and U saved, 0.98 ms
+// (1.5 PFLOP/s, 92 % of the burst matmul rate) and 1.16 ms (92 % of the sustained rate); its
+// backward pass 2.0 and 2.4 ms; int8 16384^3 2.7 ms (3.2 POP/s) and 3.2 ms; int8 gated 11008 x 4096,
+// 512 tokens 41 and 47 us, 8192 tokens 0.48 and 0.56 ms.
 // Weights fetched into L2 one ring ahead: 1 to 20 % slower. A tile's epilogue takes about 2.5 us
 // and bounds reductions shorter than 8 slabs (16384 x 4096 x 256 int8: 47 us, 3.0 TB/s).
 #include <algorithm>
@@ -490,9 +492,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
                 }
             }
             else if constexpr (I8) factors(next, first);
-            // The accumulator goes back to the MMA warp (of the pair's first CTA). All that this
-            // orders are reads of TMEM that have returned; a release would wait for the results'
-            // stores.
+            // The accumulator goes back to the MMA warp (of the pair's first CTA). The order that this
+            // needs is of tcgen05 operations alone: the reads of TMEM are complete behind their
+            // wait::ld, fence::before_thread_sync orders them before the arrival, and the MMA warp's
+            // fence::after_thread_sync its MMAs behind the barrier. That is PTX's rule for tcgen05
+            // across threads, and it asks for no release, which would wait for the results' stores too.
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(acce_bar(b), 0));
