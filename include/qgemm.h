@@ -350,9 +350,10 @@ qg_status qgemm_dense_gated(const void *X, const void *Wg, const void *Wu, void 
  * saved. dX: [M, K]; dWg, dWu: [F, K]; everything of type `dtype`.
  *     dG = dH * U * act'(G),  dU = dH * act(G)             (fp32, rounded to `dtype`)
  *     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X      (fp32 sums, rounded once)
- * In fp16, dG and dU may leave its range: they are rounded after multiplication by the power of two
- * that brings the largest finite one of both to 2^14 .. 2^15, and the sums are divided by it. Each
- * is off by half a step of `dtype` or, in fp16, by at most 2^-39 of that largest one.
+ * In fp16, dG and dU may leave its range: they are rounded after multiplication by one power of two,
+ * chosen by the largest finite one of both so that it does not overflow, and the sums are divided by
+ * it. Each is off by half a step of `dtype` or, in fp16, by at most 2^-38 of the largest finite
+ * |dH U| or |dH G|.
  * dX may be NULL, and so may dWg and dWu together; what is NULL is not computed.
  * workspace: caller-owned device memory, 256-byte aligned, at least
  * qgemm_dense_gated_backward_workspace_bytes(M, F, K) bytes, contents on entry and after the

@@ -1,6 +1,7 @@
 """Gradients whose elementwise half leaves the range of fp16 although they themselves do not: dG = dH U
 act'(G) and dU = dH act(G) go to the tensor cores in 16 bits, scaled by one power of two so that the
-largest of them lies between 2^14 and 2^15.
+largest of them (for gelu a bound at most 1.3 times the value of a positive gate) lies between 2^14 and
+2^15.
 
 Bound of one rounded value: half a step of its type relative to it, or, where it is so much smaller than
 the largest that it becomes a subnormal number after scaling, half of 2^-24 at that scale: at most
@@ -25,11 +26,22 @@ def halves(dH, G, U, act):
     return dh * u * R.slope(g, act), dh * R.value(g, act)
 
 
+def largest(dH, G, U, act):
+    """What the power of two is chosen by: the largest finite |dG| or |dU|; for gelu, of their bounds
+    with s = 17/16 / (1 + exp(-1.702 g)) >= Phi(g): |act| <= |g| s, |act'| <= min(1.13, (1 + |g|) s)."""
+    if act == "gelu":
+        dh, g, u = dH.double(), G.double(), U.double()
+        s = 17 / 16 * torch.sigmoid(1.702 * g)
+        both = dh * u * ((1 + g.abs()) * s).clamp(max=1.13), dh * g * s
+    else:
+        both = halves(dH, G, U, act)
+    return max(float(t[torch.isfinite(t)].abs().max()) for t in both)
+
+
 def reference(dH, X, Wg, Wu, G, U, act, rows=slice(None)):
     """ffn_ref.backward with the bound of rounding dG and dU at a common scale; of some tokens."""
     dt, F = X.dtype, Wg.shape[0]
-    top = max(float(t[torch.isfinite(t)].abs().max()) for t in halves(dH, G, U, act))
-    tiny = 2.0 ** -39 * top if dt == torch.float16 else 2.0 ** -134
+    tiny = 2.0 ** -39 * largest(dH, G, U, act) if dt == torch.float16 else 2.0 ** -134
     dH, X, G, U = (t[rows] for t in (dH, X, G, U))
     M = X.shape[0]
     dh, x, wg, wu, g, u = (t.double() for t in (dH, X, Wg, Wu, G, U))
@@ -119,3 +131,19 @@ def test_non_finite_stay_in_their_row_and_column(F):
 def test_all_zero():
     c = case(70, 33, 16, torch.float16, 0.0, 1.0, 1.0, 1.0)
     assert all(bool((v == 0).all()) for v in run(c, "gelu").values())
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_every_gate_alone(act):
+    """Each gate by itself decides the power of two: largest dH and U, so that too small a bound of the
+    activations (gelu's first pass takes one) overflows, and weights that bring the gradients back."""
+    K = 8
+    dH = torch.full((1, 1), 60000.0, dtype=torch.float16, device=DEV)
+    X = torch.full((1, K), 2.0 ** -20, dtype=torch.float16, device=DEV)
+    W = torch.full((1, K), 2.0 ** -20, dtype=torch.float16, device=DEV)
+    for g in torch.cat([torch.linspace(-6, 6, 193), torch.tensor([-10.0, 10.0, 30.0, 100.0])]).tolist():
+        for u in (60000.0, 0.5):
+            c = dict(dH=dH, X=X, Wg=W, Wu=W, G=torch.full_like(dH, g), U=torch.full_like(dH, u))
+            got = run(c, act)
+            for k, (ref, bound) in reference(**c, act=act).items():
+                R.check(got[k], (ref, bound), (g, u, k))
