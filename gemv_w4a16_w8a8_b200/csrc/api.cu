@@ -1291,6 +1291,6 @@ const char *qgemm_status_string(qg_status status)
     return "unknown status";
 }
 
-int qgemm_version(void) { return 200; }
+int qgemm_version(void) { return 201; }
 
 } // extern "C"
